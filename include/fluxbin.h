@@ -154,6 +154,8 @@ typedef struct fluxbin_layer_desc {
                                          fluxbin_device_status is set, no MMA is issued, tensor
                                          memory is released and the workspace is left zero-filled.
                                          INVALID_ARG without FLUXBIN_FLAG_PATH_TC. */
+#define FLUXBIN_FLAG_BF16         256u /* 8-bit operators only: their 16-bit values are bfloat16 (else fp16) */
+#define FLUXBIN_FLAG_H_FP32       512u /* fluxbin_rmsnorm_quant only: h and h_out are float32 */
 /*
  * Two execution paths compute the same layer.  The LUT path builds the 2^mu
  * signed partial sums of every activation sub-vector in shared memory and
@@ -378,6 +380,104 @@ int fluxbin_linear_static_scratch(const fluxbin_layer_desc* desc,
                                   const uint32_t* d_swords, const uint16_t* d_rs, const uint16_t* d_cs,
                                   const int32_t* d_idx, const uint16_t* d_x, int32_t B,
                                   void* d_y, uint32_t flags, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit operators
+ * ---------------------------------------------------------------------------
+ * (Additions of this library; the FluxBin pages have no counterpart.)  For
+ * what a model keeps beside its binary layers: layers left out of the
+ * binarisation (an output head, sensitive projections) at one byte per
+ * weight, and activations of any number of rows (the layers above take 16 at
+ * most), so that a prompt runs through them too.  Activations are quantised
+ * per row (token), weights per row (channel); the operators below quantise
+ * what a block feeds into such a layer and multiply.
+ *
+ *   codes and scale of a row v of N values:
+ *     a = max_n |v[n]|,  q[n] = rint(v[n] * (127 / a)),  s = a / 127
+ *   (fp32, nearest even, codes in -127..127; v[n] is about q[n] * s).
+ *   A row of zeros gets codes 0 and s = 0.  A row without a finite scale (a
+ *   NaN or an infinity in it) gets codes 0 and s = NaN, so that every product
+ *   with it is NaN.
+ *
+ * Rows may be apart: every array of rows has a pitch (ld..., in elements, at
+ * least the row's length and at most 2^40).  Arrays of codes start at a
+ * multiple of 16 bytes and have a pitch that is a multiple of 16; the bytes
+ * between two rows are neither read nor written.  Other arrays need the
+ * alignment of their elements only (16-byte aligned rows of a length that is
+ * a multiple of 8 are faster).  16-bit values are fp16, or bfloat16 with
+ * FLUXBIN_FLAG_BF16.  Outputs must not overlap each other or an input (the
+ * spans from an array's first to its last element are compared) except where
+ * said.  No workspace is needed; calls on different streams and replays of
+ * captured graphs may run at the same time.  Launches are programmatic
+ * dependent launches; every array is read and written only after the
+ * preceding kernel on the stream has completed, except as
+ * FLUXBIN_FLAG_EARLY_WEIGHTS says.
+ * N is at most 131071 (UNSUPPORTED above): the 32-bit sum of N products of
+ * two codes cannot overflow.  T == 0 returns FLUXBIN_OK without launching.
+ */
+
+/*
+ * Codes and scales of T rows of 16-bit values:  v = x.
+ *   d_x     [T][ldx], N values a row
+ *   d_q     int8 [T][ldq], d_scale float32 [T]
+ *   flags   FLUXBIN_FLAG_BF16 only
+ * N == 0 writes scales of 0.
+ * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
+ */
+int fluxbin_quant_rows(int32_t T, int32_t N, const uint16_t* d_x, int64_t ldx, int8_t* d_q, int64_t ldq,
+                       float* d_scale, uint32_t flags, void* stream);
+
+/*
+ * The gate of a LLaMA-style MLP with an 8-bit output:
+ *   v[n] = g[n] / (1 + exp(-g[n])) * u[n]
+ * in fp32 from 16-bit g and u (d_gate and d_up may be the two halves of the
+ * rows of one array).  Other arguments as for fluxbin_quant_rows.
+ * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
+ */
+int fluxbin_silu_mul_quant(int32_t T, int32_t N, const uint16_t* d_gate, int64_t ldg, const uint16_t* d_up,
+                           int64_t ldu, int8_t* d_q, int64_t ldq, float* d_scale, uint32_t flags, void* stream);
+
+/*
+ * The residual's addition and the RMS normalisation with an 8-bit output:
+ *   h' = h + delta              (rounded once to h's type; h' = h without delta)
+ *   v  = h' (.) gamma / sqrt(mean_n(h'[n]^2) + eps)
+ *   d_h      [T][ldh] 16-bit, or float32 with FLUXBIN_FLAG_H_FP32
+ *   d_delta  16-bit [T][ldd] or NULL
+ *   d_gamma  16-bit [N]
+ *   eps      >= 0, finite
+ *   d_h_out  [T][ldo] of h's type or NULL: receives h'; may be d_h itself (with ldo == ldh)
+ *   d_q, d_scale   as for fluxbin_quant_rows
+ *   flags    FLUXBIN_FLAG_BF16, FLUXBIN_FLAG_H_FP32
+ * The sum of squares is taken in fp32 in a fixed order; a row whose sum, or
+ * whose 1/rms (a row of zeros with eps == 0), is not finite has no finite
+ * scale (above).  N == 0 is BAD_SHAPE.
+ * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
+ */
+int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, const uint16_t* d_delta, int64_t ldd,
+                          const uint16_t* d_gamma, float eps, void* d_h_out, int64_t ldo, int8_t* d_q, int64_t ldq,
+                          float* d_scale, uint32_t flags, void* stream);
+
+/*
+ * The 8-bit integer product with a scale for each channel and each token:
+ *   y[t][m] (+)= xscale[t] * wscale[m] * sum_n x[t][n] * w[m][n]
+ * The sum is exact (any int8 codes, -128 among them); it is rounded to fp32
+ * once, multiplied by the scales in fp32 and rounded to y's type (with
+ * FLUXBIN_FLAG_ACCUMULATE after the addition to y).  The result does not
+ * depend on T: a token's row is the same bit for bit alone and in a batch.
+ *   M, N     output features (channels) and input features
+ *   d_w      int8 codes [M][ldw], d_wscale float32 [M]
+ *   d_x      int8 codes [T][ldx], d_xscale float32 [T]; any T >= 0
+ *   d_y      [T][ldy]: fp16, bfloat16 (FLUXBIN_FLAG_BF16) or float32 (FLUXBIN_FLAG_Y_FP32)
+ *   flags    FLUXBIN_FLAG_ACCUMULATE, FLUXBIN_FLAG_Y_FP32, FLUXBIN_FLAG_BF16 (not both types),
+ *            FLUXBIN_FLAG_EARLY_WEIGHTS (w and wscale may be read before the preceding kernel
+ *            on the stream has finished)
+ * M == 0 returns FLUXBIN_OK without launching; N == 0 is a product of zero.
+ * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
+ */
+int fluxbin_int8_linear(int32_t M, int32_t N, const int8_t* d_w, int64_t ldw, const float* d_wscale,
+                        const int8_t* d_x, int64_t ldx, const float* d_xscale, int32_t T, void* d_y, int64_t ldy,
+                        uint32_t flags, void* stream);
 
 /*
  * ---------------------------------------------------------------------------

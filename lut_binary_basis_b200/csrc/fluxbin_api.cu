@@ -9,6 +9,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "fluxbin_device.h"
 #include "fluxbin_host.h"
 #include "fluxbin_kernel.cuh"
 #include "fluxbin_tc.cuh"
@@ -860,6 +861,13 @@ int run(int32_t M, int32_t N, int mu, const BranchIn& g, const BranchIn* s, cons
 }
 
 }  // namespace
+
+int report_cuda_failure(cudaError_t e) { return cuda_fail(e); }
+
+int device_error_word(int dev, unsigned int** out) {
+    std::lock_guard<std::mutex> lock(g_tc_mu);
+    return device_error_address(dev, out);
+}
 
 int linear_impl(const fluxbin_layer_desc* desc, const uint32_t* d_words, const uint16_t* d_r, const uint16_t* d_c,
                 const uint32_t* d_swords, const uint16_t* d_rs, const uint16_t* d_cs, const int32_t* d_idx,

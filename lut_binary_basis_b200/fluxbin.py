@@ -24,6 +24,8 @@ FLAG_PATH_LUT = 8
 FLAG_PATH_TC = 16
 FLAG_TEST_WAIT_TIMEOUT = 32
 FLAG_SEPARATE_TABLES = 64
+FLAG_BF16 = 256
+FLAG_H_FP32 = 512
 
 STATUS = {0: "FLUXBIN_OK", -1: "FLUXBIN_ERR_INVALID_ARG", -2: "FLUXBIN_ERR_BAD_SHAPE",
           -3: "FLUXBIN_ERR_MISALIGNED", -4: "FLUXBIN_ERR_UNSUPPORTED", -5: "FLUXBIN_ERR_SMEM_BUDGET",
@@ -79,6 +81,11 @@ def lib():
             L.fluxbin_linear.argtypes = [P, P, P, P, P, P, P, P, P, i32, P, u32, P, sz, P]
             L.fluxbin_linear_static_scratch.argtypes = [P, P, P, P, P, P, P, P, P, i32, P, u32, P]
             L.fluxbin_linear_rmsnorm.argtypes = [P, P, P, P, P, P, P, P, P, P, ctypes.c_float, P, P, u32, P, sz, P]
+            i64 = ctypes.c_int64
+            L.fluxbin_quant_rows.argtypes = [i32, i32, P, i64, P, i64, P, u32, P]
+            L.fluxbin_silu_mul_quant.argtypes = [i32, i32, P, i64, P, i64, P, i64, P, u32, P]
+            L.fluxbin_rmsnorm_quant.argtypes = [i32, i32, P, i64, P, i64, P, ctypes.c_float, P, i64, P, i64, P, u32, P]
+            L.fluxbin_int8_linear.argtypes = [i32, i32, P, i64, P, P, i64, P, i32, P, i64, u32, P]
             L.fluxbin_device_status.argtypes = [ctypes.POINTER(u32)]
             L.fluxbin_fit.argtypes = [i32, i32, i32, i32, i32, P, P, P, P, P, P]
             L.fluxbin_fit_hybrid.argtypes = [i32, i32, i32, i32, i32, i32, P, i32, i32, P, P, P, P, P, P, P, P, P]
@@ -86,7 +93,8 @@ def lib():
                       "fluxbin_layer_workspace_bytes", "fluxbin_lut_gemv",
                       "fluxbin_linear", "fluxbin_linear_static_scratch", "fluxbin_linear_rmsnorm",
                       "fluxbin_device_status", "fluxbin_fit",
-                      "fluxbin_fit_hybrid"):
+                      "fluxbin_fit_hybrid", "fluxbin_quant_rows", "fluxbin_silu_mul_quant",
+                      "fluxbin_rmsnorm_quant", "fluxbin_int8_linear"):
                 getattr(L, f).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -323,3 +331,186 @@ def new_workspace(M: int, B: int, device="cuda"):
     import torch
     n = max(fluxbin_workspace_bytes(M, B), 256)
     return torch.zeros(n // 4, dtype=torch.int32, device=device)
+
+
+# ----------------------------------------------------------------------------
+# 8-bit operators
+# ----------------------------------------------------------------------------
+
+def fluxbin_quant_rows(T: int, N: int, x, ldx: int, q, ldq: int, scale, flags: int = 0, stream=None) -> None:
+    """Codes and scales of T rows of 16-bit values (include/fluxbin.h)."""
+    _check(lib().fluxbin_quant_rows(T, N, _dptr(x), ldx, _dptr(q), ldq, _dptr(scale), flags, _stream(stream)),
+           "fluxbin_quant_rows")
+
+
+def fluxbin_silu_mul_quant(T: int, N: int, gate, ldg: int, up, ldu: int, q, ldq: int, scale, flags: int = 0,
+                           stream=None) -> None:
+    """Codes and scales of silu(gate) * up (include/fluxbin.h)."""
+    _check(lib().fluxbin_silu_mul_quant(T, N, _dptr(gate), ldg, _dptr(up), ldu, _dptr(q), ldq, _dptr(scale), flags,
+                                        _stream(stream)), "fluxbin_silu_mul_quant")
+
+
+def fluxbin_rmsnorm_quant(T: int, N: int, h, ldh: int, delta, ldd: int, gamma, eps: float, h_out, ldo: int, q,
+                          ldq: int, scale, flags: int = 0, stream=None) -> None:
+    """Codes and scales of the RMS normalisation of h + delta (include/fluxbin.h)."""
+    _check(lib().fluxbin_rmsnorm_quant(T, N, _dptr(h), ldh, _dptr(delta), ldd, _dptr(gamma), float(eps),
+                                       _dptr(h_out), ldo, _dptr(q), ldq, _dptr(scale), flags, _stream(stream)),
+           "fluxbin_rmsnorm_quant")
+
+
+def fluxbin_int8_linear(M: int, N: int, w, ldw: int, wscale, x, ldx: int, xscale, T: int, y, ldy: int,
+                        flags: int = 0, stream=None) -> None:
+    """y (+)= the 8-bit integer product with token and channel scales (include/fluxbin.h)."""
+    _check(lib().fluxbin_int8_linear(M, N, _dptr(w), ldw, _dptr(wscale), _dptr(x), ldx, _dptr(xscale), T, _dptr(y),
+                                     ldy, flags, _stream(stream)), "fluxbin_int8_linear")
+
+
+def _pitch16(n: int) -> int:
+    return -(-n // 16) * 16
+
+
+def _matrix(t, name: str, shape, dtypes, device) -> int:
+    """Checks a row-major matrix on ``device`` and returns its row pitch."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    rows, cols = t.shape
+    row, col = t.stride()
+    if cols > 1 and col != 1:
+        raise ValueError(f"{name} is not row-major (strides {tuple(t.stride())})")
+    # the pitch of a single row, or of empty ones, says nothing
+    return row if rows > 1 and cols > 0 else _pitch16(cols)
+
+
+def _vector(t, name: str, n: int, dtypes, device) -> None:
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({n},)")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _on_device(device, call, *args, stream=None) -> None:
+    """Runs a device call with the tensors' own device current, on ``stream``
+    or that device's current stream."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        call(*args, _stream(stream))
+        return
+    with torch.cuda.device(device):
+        call(*args, _stream(stream))
+
+
+def _types16():
+    import torch
+    return torch.float16, torch.bfloat16
+
+
+class QuantRows:
+    """T rows of 8-bit codes with one scale each: the left operand of
+    ``Int8Layer.linear``, filled by one of the quantising operators.
+
+    ``q`` int8 [T][N] (16-byte aligned, pitch a multiple of 16), ``scale``
+    float32 [T], both on one CUDA device and owned by the caller."""
+
+    __slots__ = ("q", "scale", "T", "N", "ldq", "device")
+
+    def __init__(self, q, scale):
+        import torch
+        if q.dim() != 2:
+            raise ValueError("q is not a matrix")
+        self.q, self.scale, self.device = q, scale, q.device
+        self.T, self.N = q.shape
+        self.ldq = _matrix(q, "q", q.shape, (torch.int8,), q.device)
+        _vector(scale, "scale", self.T, (torch.float32,), q.device)
+
+    @classmethod
+    def empty(cls, T: int, N: int, device="cuda") -> "QuantRows":
+        import torch
+        q = torch.empty((T, _pitch16(N)), dtype=torch.int8, device=device)[:, :N]
+        return cls(q, torch.empty(T, dtype=torch.float32, device=device))
+
+    def rows(self, T: int) -> "QuantRows":
+        """The first T rows (sharing memory)."""
+        return QuantRows(self.q[:T], self.scale[:T])
+
+    def quantize(self, x, stream=None) -> None:
+        """Codes and scales of the rows of x (fp16 or bf16 [T][N])."""
+        e = _types16()
+        ldx = _matrix(x, "x", (self.T, self.N), e, self.device)
+        _on_device(self.device, fluxbin_quant_rows, self.T, self.N, x, ldx, self.q, self.ldq, self.scale,
+                   FLAG_BF16 if x.dtype == e[1] else 0, stream=stream)
+
+    def silu_mul(self, gate, up, stream=None) -> None:
+        """Codes and scales of silu(gate) * up (both fp16 or both bf16 [T][N])."""
+        e = _types16()
+        ldg = _matrix(gate, "gate", (self.T, self.N), e, self.device)
+        ldu = _matrix(up, "up", (self.T, self.N), (gate.dtype,), self.device)
+        _on_device(self.device, fluxbin_silu_mul_quant, self.T, self.N, gate, ldg, up, ldu, self.q, self.ldq,
+                   self.scale, FLAG_BF16 if gate.dtype == e[1] else 0, stream=stream)
+
+    def rmsnorm(self, h, gamma, eps: float, delta=None, h_out=None, stream=None) -> None:
+        """Codes and scales of rmsnorm(h + delta) * gamma; ``h_out`` (may be h)
+        receives h + delta.  gamma and delta are both fp16 or both bf16; h and
+        h_out have that type or float32."""
+        import torch
+        e = _types16()
+        _vector(gamma, "gamma", self.N, e, self.device)
+        ldh = _matrix(h, "h", (self.T, self.N), (gamma.dtype, torch.float32), self.device)
+        ldd = 0 if delta is None else _matrix(delta, "delta", (self.T, self.N), (gamma.dtype,), self.device)
+        ldo = 0 if h_out is None else _matrix(h_out, "h_out", (self.T, self.N), (h.dtype,), self.device)
+        flags = (FLAG_BF16 if gamma.dtype == e[1] else 0) | (FLAG_H_FP32 if h.dtype == torch.float32 else 0)
+        _on_device(self.device, fluxbin_rmsnorm_quant, self.T, self.N, h, ldh, delta, ldd, gamma, eps, h_out, ldo,
+                   self.q, self.ldq, self.scale, flags, stream=stream)
+
+
+class Int8Layer:
+    """A linear layer of 8-bit weights with one scale per channel.
+
+    ``w`` int8 [M][N] (16-byte aligned, pitch a multiple of 16), ``scale``
+    float32 [M], both on one CUDA device and owned by the caller."""
+
+    __slots__ = ("w", "scale", "M", "N", "ldw", "device")
+
+    def __init__(self, w, scale):
+        import torch
+        if w.dim() != 2:
+            raise ValueError("w is not a matrix")
+        self.w, self.scale, self.device = w, scale, w.device
+        self.M, self.N = w.shape
+        self.ldw = _matrix(w, "w", w.shape, (torch.int8,), w.device)
+        _vector(scale, "scale", self.M, (torch.float32,), w.device)
+
+    @classmethod
+    def from_host(cls, W: np.ndarray, device="cuda") -> "Int8Layer":
+        """Quantise a dense host matrix W [M][N] per row (the formula of the
+        8-bit operators, in fp64) and copy it to ``device``."""
+        import torch
+        W = np.asarray(W, dtype=np.float64)
+        M, N = W.shape
+        if not np.all(np.isfinite(W)):
+            raise ValueError("W has a NaN or an infinity in it")
+        a = np.abs(W).max(axis=1, initial=0.0)
+        q = np.zeros((M, _pitch16(N)), np.int8)
+        q[:, :N] = np.rint(W * np.divide(127.0, a, out=np.zeros(M), where=a > 0)[:, None])
+        return cls(torch.from_numpy(q).to(device)[:, :N], torch.from_numpy((a / 127.0).astype(np.float32)).to(device))
+
+    def linear(self, rows: QuantRows, y, flags: int = 0, stream=None) -> None:
+        """y (+)= W x for rows x; y is fp16, bf16 or float32 [T][M].  flags:
+        FLAG_ACCUMULATE, FLAG_EARLY_WEIGHTS (y's type is read off y)."""
+        import torch
+        e = _types16()
+        if rows.N != self.N or rows.device != self.device:
+            raise ValueError(f"rows of {rows.N} codes on {rows.device} for a layer of {self.N} on {self.device}")
+        ldy = _matrix(y, "y", (rows.T, self.M), (*e, torch.float32), self.device)
+        flags |= FLAG_BF16 if y.dtype == e[1] else FLAG_Y_FP32 if y.dtype == torch.float32 else 0
+        _on_device(self.device, fluxbin_int8_linear, self.M, self.N, self.w, self.ldw, self.scale, rows.q, rows.ldq,
+                   rows.scale, rows.T, y, ldy, flags, stream=stream)
