@@ -401,7 +401,7 @@ int fluxbin_linear_static_scratch(const fluxbin_layer_desc* desc,
  *   with it is NaN.
  *
  * Rows may be apart: every array of rows has a pitch (ld..., in elements, at
- * least the row's length and at most 2^40).  Arrays of codes start at a
+ * least the row's length and at most 2^39).  Arrays of codes start at a
  * multiple of 16 bytes and have a pitch that is a multiple of 16; the bytes
  * between two rows are neither read nor written.  Other arrays need the
  * alignment of their elements only (16-byte aligned rows of a length that is
@@ -470,8 +470,10 @@ int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, co
  *   d_x      int8 codes [T][ldx], d_xscale float32 [T]; any T >= 0
  *   d_y      [T][ldy]: fp16, bfloat16 (FLUXBIN_FLAG_BF16) or float32 (FLUXBIN_FLAG_Y_FP32)
  *   flags    FLUXBIN_FLAG_ACCUMULATE, FLUXBIN_FLAG_Y_FP32, FLUXBIN_FLAG_BF16 (not both types),
- *            FLUXBIN_FLAG_EARLY_WEIGHTS (w and wscale may be read before the preceding kernel
- *            on the stream has finished)
+ *            FLUXBIN_FLAG_EARLY_WEIGHTS (w may be read before the preceding kernel on the
+ *            stream has finished), FLUXBIN_FLAG_TEST_WAIT_TIMEOUT (test hook: the kernel's
+ *            copies are never issued and its waits give up after a few polls: the outputs
+ *            become NaN and bit 0 of fluxbin_device_status is set)
  * M == 0 returns FLUXBIN_OK without launching; N == 0 is a product of zero.
  * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
  */

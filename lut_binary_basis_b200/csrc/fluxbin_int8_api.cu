@@ -2,11 +2,16 @@
 // of a kernel and the launch.  Declarations and the full contract are in
 // include/fluxbin.h.
 #include <cmath>
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "../../include/fluxbin.h"
 #include "fluxbin_device.h"
 #include "fluxbin_int8.cuh"
+#include "fluxbin_int8_tc.cuh"
 #include "fluxbin_quant.cuh"
 
 namespace fluxbin {
@@ -14,7 +19,7 @@ namespace {
 
 constexpr int32_t kInt8MaxN = 131071;   // 128 * 128 * N < 2^31
 
-constexpr int64_t kMaxPitch = (int64_t)1 << 40;   // beyond any device memory: offsets stay far from 2^63
+constexpr int64_t kMaxPitch = (int64_t)1 << 39;   // beyond any device memory: offsets stay far from 2^63
 
 // A row pitch (in elements) that rows of n elements can have.
 bool bad_pitch(int64_t ld, int64_t n) { return ld < n || ld > kMaxPitch; }
@@ -35,17 +40,24 @@ bool overlap(const Rows& a, const Rows& b) {
 }
 
 template <typename K, typename... Args>
-int launch(K kernel, dim3 grid, dim3 block, size_t smem, void* stream, const Args&... args) {
+int launch(K kernel, dim3 grid, dim3 block, size_t smem, int cluster, void* stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e == cudaSuccess ? FLUXBIN_OK : report_cuda_failure(e);
 }
@@ -129,7 +141,124 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     } else {
         fn = bf ? pick_quant<KIND, __nv_bfloat16, __nv_bfloat16>(vpt, vec) : pick_quant<KIND, __half, __half>(vpt, vec);
     }
-    return launch(fn, dim3((unsigned)((T + rpc - 1) / rpc)), dim3((unsigned)tpr, (unsigned)rpc), 0, stream, a);
+    return launch(fn, dim3((unsigned)((T + rpc - 1) / rpc)), dim3((unsigned)tpr, (unsigned)rpc), 0, 1, stream, a);
+}
+
+// ---------------------------------------------------------------------------
+// The integer product
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxDevices = 64;
+std::mutex g_int8_mu;
+
+struct Int8Device {
+    bool ready = false;
+    int sm_count = 0;
+    unsigned int* err = nullptr;
+} g_int8_dev[kMaxDevices];
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn g_encode = nullptr;
+
+using Int8TcFn = void (*)(CUtensorMap, CUtensorMap, Int8TcArgs);
+using Int8EmptyFn = void (*)(Int8Args);
+
+template <typename Y>
+Int8TcFn pick_tc(bool acc) { return acc ? &fluxbin_int8_tc_kernel<Y, true> : &fluxbin_int8_tc_kernel<Y, false>; }
+Int8TcFn pick_int8_tc(uint32_t flags) {
+    const bool acc = (flags & kInt8Accumulate) != 0;
+    return (flags & kInt8YFp32) ? pick_tc<float>(acc) : (flags & kInt8Bf16) ? pick_tc<__nv_bfloat16>(acc) : pick_tc<__half>(acc);
+}
+template <typename Y>
+Int8EmptyFn pick_empty(bool acc) { return acc ? &fluxbin_int8_empty_kernel<Y, true> : &fluxbin_int8_empty_kernel<Y, false>; }
+
+constexpr int kI8MaxSmem = 227 * 1024;
+
+// Per-device set-up of the product's kernels: the error word, the number of
+// SMs, the opt-in to their shared memory; once the tensor-map encoder.
+int int8_device(Int8Device* out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return report_cuda_failure(e);
+    if (dev < 0 || dev >= kMaxDevices) return FLUXBIN_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_int8_mu);
+    Int8Device& d = g_int8_dev[dev];
+    if (!d.ready) {
+        if (!g_encode) {
+            void* fn = nullptr;
+            cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+            e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+            if (e != cudaSuccess) return report_cuda_failure(e);
+            if (q != cudaDriverEntryPointSuccess || !fn) return report_cuda_failure(cudaErrorSymbolNotFound);
+            g_encode = reinterpret_cast<EncodeFn>(fn);
+        }
+        if ((e = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+            return report_cuda_failure(e);
+        for (const uint32_t f : {0u, kInt8YFp32, kInt8Bf16})
+            for (const uint32_t acc : {0u, kInt8Accumulate})
+                if ((e = cudaFuncSetAttribute(pick_int8_tc(f | acc), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              kI8MaxSmem)) != cudaSuccess)
+                    return report_cuda_failure(e);
+        const int st = device_error_word(dev, &d.err);
+        if (st != FLUXBIN_OK) return st;
+        d.ready = true;
+    }
+    *out = d;
+    return FLUXBIN_OK;
+}
+
+// Rows of codes as a tensor map: boxes of one swizzle row of K by `box` rows.
+int encode_rows(CUtensorMap* map, const int8_t* base, int64_t rows, int64_t N, int64_t ld, int box) {
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t boxes[2] = {(cuuint32_t)kI8K, (cuuint32_t)box};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, boxes,
+                                steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FLUXBIN_OK : report_cuda_failure(cudaErrorInvalidValue);
+}
+
+int run_int8(const Int8Args& p, void* stream) {
+    const bool acc = (p.flags & kInt8Accumulate) != 0;
+    if (p.N == 0) {
+        const int64_t blocks = ((int64_t)p.T * p.M + 255) / 256;
+        if (blocks > INT32_MAX) return FLUXBIN_ERR_UNSUPPORTED;
+        Int8EmptyFn fn = (p.flags & kInt8YFp32) ? pick_empty<float>(acc)
+                         : (p.flags & kInt8Bf16) ? pick_empty<__nv_bfloat16>(acc) : pick_empty<__half>(acc);
+        return launch(fn, dim3((unsigned)blocks), dim3(256), 0, 1, stream, p);
+    }
+    Int8Device d;
+    int st = int8_device(&d);
+    if (st != FLUXBIN_OK) return st;
+    Int8TcArgs a = {};
+    a.p = p;
+    a.kblocks = (p.N + kI8K - 1) / kI8K;
+    // token tiles of equal size, a multiple of 16
+    const int tiles_t = (p.T + kI8MaxBn - 1) / kI8MaxBn;
+    a.bn = (((p.T + tiles_t - 1) / tiles_t) + 15) / 16 * 16;
+    a.tiles_t = tiles_t;
+    const int64_t tiles = (int64_t)tiles_t * ((p.M + kI8Rows - 1) / kI8Rows);
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * d.sm_count && a.kblocks / (splits * 2) >= 2) splits *= 2;
+    a.splits = splits;
+    const int stage = int8_stage_bytes(a.bn);
+    const int per_cta = a.kblocks / splits + 1;
+    a.stages = std::min(std::min(kI8MaxStages, per_cta), ((a.bn <= 64 ? 112 * 1024 : kI8MaxSmem) - kI8RingOff) / stage);
+    if (splits > 1) a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
+    a.tmem_cols = 32;
+    while ((int)a.tmem_cols < a.bn) a.tmem_cols *= 2;
+    a.test_stall = (p.flags & FLUXBIN_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
+    a.spin_limit = a.test_stall ? kI8TestSpinLimit : kI8SpinLimit;
+    a.err = d.err;
+    if (tiles * splits > INT32_MAX) return FLUXBIN_ERR_UNSUPPORTED;
+    CUtensorMap mw, mx;
+    if ((st = encode_rows(&mw, p.w, p.M, p.N, p.ldw, kI8Rows)) != FLUXBIN_OK) return st;
+    if ((st = encode_rows(&mx, p.x, p.T, p.N, p.ldx, a.bn)) != FLUXBIN_OK) return st;
+    return launch(pick_int8_tc(p.flags), dim3((unsigned)(tiles * splits)), dim3(128),
+                  (size_t)(kI8RingOff + a.stages * stage), splits, stream, mw, mx, a);
 }
 
 }  // namespace
@@ -175,7 +304,8 @@ int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, co
 int fluxbin_int8_linear(int32_t M, int32_t N, const int8_t* d_w, int64_t ldw, const float* d_wscale,
                         const int8_t* d_x, int64_t ldx, const float* d_xscale, int32_t T, void* d_y, int64_t ldy,
                         uint32_t flags, void* stream) {
-    if (flags & ~(FLUXBIN_FLAG_ACCUMULATE | FLUXBIN_FLAG_Y_FP32 | FLUXBIN_FLAG_EARLY_WEIGHTS | FLUXBIN_FLAG_BF16))
+    if (flags & ~(FLUXBIN_FLAG_ACCUMULATE | FLUXBIN_FLAG_Y_FP32 | FLUXBIN_FLAG_EARLY_WEIGHTS | FLUXBIN_FLAG_BF16 |
+                  FLUXBIN_FLAG_TEST_WAIT_TIMEOUT))
         return FLUXBIN_ERR_INVALID_ARG;
     if ((flags & FLUXBIN_FLAG_Y_FP32) && (flags & FLUXBIN_FLAG_BF16)) return FLUXBIN_ERR_INVALID_ARG;
     if (M < 0 || N < 0 || T < 0 || bad_pitch(ldw, N) || bad_pitch(ldx, N) || bad_pitch(ldy, M))
@@ -204,9 +334,7 @@ int fluxbin_int8_linear(int32_t M, int32_t N, const int8_t* d_w, int64_t ldw, co
     a.N = N;
     a.T = T;
     a.flags = flags;
-    const int64_t tm = ((int64_t)M + kInt8Tile - 1) / kInt8Tile, tt = ((int64_t)T + kInt8Tile - 1) / kInt8Tile;
-    if (tt > 65535) return FLUXBIN_ERR_UNSUPPORTED;
-    return launch(&fluxbin_int8_kernel, dim3((unsigned)tm, (unsigned)tt), dim3(256), 0, stream, a);
+    return run_int8(a, stream);
 }
 
 }  // extern "C"

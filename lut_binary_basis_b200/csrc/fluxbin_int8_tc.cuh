@@ -1,0 +1,281 @@
+// The 8-bit integer product on the fifth-generation tensor cores (sm_100a).
+//
+//   acc[m][t] = sum_n wq[m][n] xq[t][n],  y[t][m] (+)= acc * (sx[t] * sw[m])
+//
+// The weights are the matrix instruction's A operand (128 channels a tile, so
+// channels lie along the tensor memory's lanes and a warp stores 32
+// consecutive channels of a token at once) and the tokens its B operand: a
+// tile of `bn` tokens, a multiple of 16 up to 256, fits the batch at hand
+// without wasting operand loads on padding.  Both are K-major rows of codes,
+// copied by TMA with the 128-byte swizzle, 128 codes of K a stage; rows and
+// codes beyond the arrays' ends arrive as zeros.
+//
+// Split of K: with few tiles the stages of a tile are shared out over the
+// CTAs of a cluster.  Every CTA leaves its partial sums in its own shared
+// memory, and each then adds its share of the tokens over all of them through
+// distributed shared memory: integer sums, so the split changes no bit.  A
+// CTA releases its tensor memory before it waits for the others (none holds
+// tensor memory while it waits for one that may be waiting for some).
+//
+// Roles: thread 0 of warp 0 issues the copies, thread 0 of warp 1 the matrix
+// instructions; a ring of stages with full and empty mbarriers lies between
+// them.  All four warps then empty the accumulators.  Every wait is bounded:
+// one that gives up sets bit 0 of the device error word, and the CTA's sums
+// are replaced by NaN outputs.
+#pragma once
+
+#include <cuda.h>
+
+#include "fluxbin_int8.cuh"
+#include "fluxbin_tc.cuh"
+
+namespace fluxbin {
+
+constexpr int kI8Rows = 128;                     // channels of a tile
+constexpr int kI8K = 128;                        // codes of K a stage (one swizzle row)
+constexpr int kI8MaxBn = 256;
+constexpr int kI8MaxStages = 12;
+constexpr uint32_t kI8SpinLimit = 1u << 22;      // polls (each may suspend for microseconds) before a wait fails
+constexpr uint32_t kI8TestSpinLimit = 64u;
+
+struct Int8TcArgs {
+    Int8Args p;
+    int32_t bn;           // tokens of a tile
+    int32_t kblocks;      // stages of K
+    int32_t splits;       // CTAs (of one cluster) that share a tile
+    int32_t stages;       // ring length
+    int32_t tiles_t;      // token tiles
+    uint32_t tmem_cols;
+    uint32_t spin_limit;
+    int32_t test_stall;   // test hook: no copy is issued
+    unsigned int* err;
+};
+
+// Byte offset of the ring behind the barriers (1024-byte atoms).
+constexpr int kI8RingOff = 1024;
+__host__ __device__ constexpr int int8_stage_bytes(int bn) { return kI8Rows * kI8K + bn * kI8K; }
+
+// Instruction descriptor of the 8-bit integer kind: 32-bit integer
+// accumulator, signed A and B, both K-major.
+__device__ __forceinline__ uint32_t int8_idesc(int m, int n) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void int8_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+}
+
+__device__ __forceinline__ void int8_tma(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void int8_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void int8_ld16(uint32_t taddr, int (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void int8_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ int ld_dsmem(uint32_t addr, int rank) {
+    int v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+        "ld.shared::cluster.b32 %0, [a];\n\t}"
+        : "=r"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
+// Writes 16 tokens t0 .. t0+15 (fewer at the end of T) of channel m, every
+// load before the first store.
+template <typename Y, bool ACC>
+__device__ __forceinline__ void int8_store16(const Int8Args& p, int64_t t0, int m, float sw, const int (&acc)[16],
+                                             bool ok) {
+    Y* y = static_cast<Y*>(p.y) + t0 * p.ldy + m;
+    const int n = (int)(p.T - t0 < 16 ? p.T - t0 : 16);
+    float s[16], old[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        s[j] = j < n ? __ldg(p.sx + t0 + j) : 0.f;
+        if (ACC) old[j] = j < n ? to_f32(y[j * p.ldy]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float v = int8_value(acc[j], s[j], sw);
+        if (!ok) v = __int_as_float(0x7fc00000);
+        if (ACC) v += old[j];
+        if (j < n) y[j * p.ldy] = from_f32<Y>(v);
+    }
+}
+
+template <typename Y, bool ACC>
+__global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                              const __grid_constant__ CUtensorMap map_x,
+                                                              const __grid_constant__ Int8TcArgs a) {
+    const Int8Args& p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sb = smem_base();
+    const uint32_t full0 = sb, empty0 = sb + 8 * kI8MaxStages, done = sb + 16 * kI8MaxStages;
+    constexpr uint32_t kSlot = 16 * kI8MaxStages + 8, kFailed = kSlot + 4;
+    const uint32_t ring = sb + kI8RingOff;
+    const uint32_t stage_bytes = (uint32_t)int8_stage_bytes(a.bn);
+
+    const int rank = (int)(blockIdx.x % (unsigned)a.splits);
+    const unsigned tile = blockIdx.x / (unsigned)a.splits;
+    const int tile_t = (int)(tile % (unsigned)a.tiles_t), tile_m = (int)(tile / (unsigned)a.tiles_t);
+    const int kb0 = (int)((int64_t)a.kblocks * rank / a.splits), kb1 = (int)((int64_t)a.kblocks * (rank + 1) / a.splits);
+    const int nk = kb1 - kb0;
+
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSlot),
+                     "r"(a.tmem_cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            tc_mbar_init(full0 + 8 * s, 1);
+            tc_mbar_init(empty0 + 8 * s, 1);
+        }
+        tc_mbar_init(done, 1);
+        smem_at<uint32_t>(kFailed) = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t tmem = smem_at<const uint32_t>(kSlot);
+    const bool aligned = (sb & 1023u) == 0;
+
+    if (warp == 0 && lane == 0 && aligned) {
+        // ---- copies ----
+        bool ok = true;
+        const bool early = (p.flags & kInt8Early) != 0;
+        const int ahead = nk < a.stages ? nk : a.stages;
+        const int nload = a.test_stall ? 0 : nk;
+        int i = 0;
+        if (early && nload) {
+            // the ring's first weights before the preceding kernel has finished
+            for (int s = 0; s < ahead; ++s) {
+                int8_expect(full0 + 8 * s, stage_bytes);
+                int8_tma(ring + s * stage_bytes, &map_w, (kb0 + s) * kI8K, tile_m * kI8Rows, full0 + 8 * s);
+            }
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        for (; i < nload && ok; ++i) {
+            const int s = i % a.stages;
+            const uint32_t dst = ring + s * stage_bytes;
+            if (i >= a.stages) ok = tc_mbar_wait(empty0 + 8 * s, (uint32_t)(i / a.stages - 1) & 1u, a.spin_limit);
+            if (!ok) break;
+            if (!early || i >= ahead) {
+                int8_expect(full0 + 8 * s, stage_bytes);
+                int8_tma(dst, &map_w, (kb0 + i) * kI8K, tile_m * kI8Rows, full0 + 8 * s);
+            }
+            int8_tma(dst + kI8Rows * kI8K, &map_x, (kb0 + i) * kI8K, tile_t * a.bn, full0 + 8 * s);
+        }
+        if (!ok) {
+            atomicOr(a.err, 1u);
+            smem_at<uint32_t>(kFailed) = 1u;
+        }
+        // copies in flight land before the CTA ends: the last fill of every stage
+        for (int k = i > a.stages ? i - a.stages : 0; k < i; ++k)
+            (void)tc_mbar_wait(full0 + 8 * (k % a.stages), (uint32_t)(k / a.stages) & 1u, kI8SpinLimit);
+    } else if (warp == 1 && lane == 0 && aligned) {
+        // ---- matrix instructions ----
+        const uint32_t idesc = int8_idesc(kI8Rows, a.bn);
+        bool ok = true;
+        int i = 0;
+        for (; i < nk && ok; ++i) {
+            const int s = i % a.stages;
+            ok = tc_mbar_wait(full0 + 8 * s, (uint32_t)(i / a.stages) & 1u, a.spin_limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
+            const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) int8_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
+            tc_commit(empty0 + 8 * s);
+        }
+        tc_commit(done);   // every instruction issued above has finished (at once when there is none)
+        if (!ok) {
+            atomicOr(a.err, 1u);
+            smem_at<uint32_t>(kFailed) = 1u;
+        }
+    }
+    __syncwarp();
+    // every thread waits for the accumulators; the full limit even under the
+    // test hook, since nothing may release them under running instructions
+    const bool drained = aligned ? tc_mbar_wait(done, 0u, kI8SpinLimit) : true;
+    if (tid == 0 && (!drained || !aligned)) {
+        atomicOr(a.err, drained ? 1u : 2u);
+        smem_at<uint32_t>(kFailed) = 1u;
+    }
+    // outputs are written (and scales read) after the preceding kernel
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+    tc_fence_after();
+    const bool ok = drained && smem_at<const volatile uint32_t>(kFailed) == 0u;
+
+    const int row = warp * 32 + lane;            // this thread's lane of the accumulators
+    const int m = tile_m * kI8Rows + row;
+    const int64_t t0 = (int64_t)tile_t * a.bn;
+    const uint32_t acc0 = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t red = ring;                   // [bn][128] partial sums (every stage has been consumed)
+    if (a.splits == 1) {
+        const float sw = m < p.M ? p.sw[m] : 0.f;
+        for (int c = 0; c < a.bn; c += 16) {
+            int v[16];
+            int8_ld16(acc0 + (uint32_t)c, v);
+            tc_wait_ld();
+            if (m < p.M && t0 + c < p.T) int8_store16<Y, ACC>(p, t0 + c, m, sw, v, ok);
+        }
+    } else {
+        for (int c = 0; c < a.bn; c += 16) {
+            int v[16];
+            int8_ld16(acc0 + (uint32_t)c, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) smem_at<int>(kI8RingOff + ((c + j) * kI8Rows + row) * 4) = v[j];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1 && drained) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols));
+    }
+    if (a.splits > 1) {
+        int8_cluster_sync();
+        // this CTA's share of the tile's tokens, added over the cluster
+        bool all_ok = true;
+        for (int r = 0; r < a.splits; ++r) all_ok = all_ok && ld_dsmem(sb + kFailed, r) == 0;
+        const float sw = m < p.M ? p.sw[m] : 0.f;
+        const int groups = a.bn / 16, g0 = groups * rank / a.splits, g1 = groups * (rank + 1) / a.splits;
+        for (int c = 16 * g0; c < 16 * g1 && t0 + c < p.T; c += 16) {
+            int v[16] = {};
+            for (int r = 0; r < a.splits; ++r) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += ld_dsmem(red + (uint32_t)(((c + j) * kI8Rows + row) * 4), r);
+            }
+            if (m < p.M) int8_store16<Y, ACC>(p, t0 + c, m, sw, v, all_ok);
+        }
+        int8_cluster_sync();                     // the others have read this CTA's sums
+    }
+}
+
+}  // namespace fluxbin

@@ -201,3 +201,15 @@ def test_many_tokens():
     layer.linear(rows, y)
     check(y, ref.linear(w, np.full(M, 2.0 ** -8, np.float32), x, np.ones(T, np.float32)), "fp16")
     assert bool((buf[:, 999] == 0).all()) and bool((buf[:, 1000 + M] == 0).all())
+
+
+@pytest.mark.parametrize("T,M,N", [(20, 300, 4096), (200, 2000, 1000), (600, 4096, 512)])
+def test_waits_that_give_up(T, M, N):
+    """The bounded waits' give-up path: NaN outputs, the status bit (read and
+    cleared), and a correct next call."""
+    layer, rows, want = problem(T, M, N, seed=9)
+    y = run(layer, rows, "fp32", flags=fluxbin.FLAG_TEST_WAIT_TIMEOUT)
+    assert bool(torch.isnan(y).all())
+    assert fluxbin.fluxbin_device_status() & 1
+    assert fluxbin.fluxbin_device_status() == 0
+    check(run(layer, rows, "fp32"), want, "fp32")
