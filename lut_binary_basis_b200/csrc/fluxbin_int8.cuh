@@ -24,6 +24,7 @@ struct Int8Args {
     int64_t ldw, ldx, ldy;
     int32_t M, N, T;
     uint32_t flags;
+    int32_t vec4;         // rows of y allow accesses of four elements
 };
 
 constexpr uint32_t kInt8Accumulate = 1u, kInt8YFp32 = 2u, kInt8Early = 4u, kInt8Bf16 = 256u;

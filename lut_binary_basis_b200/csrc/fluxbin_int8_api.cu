@@ -12,6 +12,7 @@
 #include "fluxbin_device.h"
 #include "fluxbin_int8.cuh"
 #include "fluxbin_int8_tc.cuh"
+#include "fluxbin_int8_tc2.cuh"
 #include "fluxbin_quant.cuh"
 
 namespace fluxbin {
@@ -171,6 +172,13 @@ Int8TcFn pick_int8_tc(uint32_t flags) {
     const bool acc = (flags & kInt8Accumulate) != 0;
     return (flags & kInt8YFp32) ? pick_tc<float>(acc) : (flags & kInt8Bf16) ? pick_tc<__nv_bfloat16>(acc) : pick_tc<__half>(acc);
 }
+using Int8PairFn = void (*)(CUtensorMap, CUtensorMap, Int8PairArgs);
+template <typename Y>
+Int8PairFn pick_pair(bool acc) { return acc ? &fluxbin_int8_pair_kernel<Y, true> : &fluxbin_int8_pair_kernel<Y, false>; }
+Int8PairFn pick_int8_pair(uint32_t flags) {
+    const bool acc = (flags & kInt8Accumulate) != 0;
+    return (flags & kInt8YFp32) ? pick_pair<float>(acc) : (flags & kInt8Bf16) ? pick_pair<__nv_bfloat16>(acc) : pick_pair<__half>(acc);
+}
 template <typename Y>
 Int8EmptyFn pick_empty(bool acc) { return acc ? &fluxbin_int8_empty_kernel<Y, true> : &fluxbin_int8_empty_kernel<Y, false>; }
 
@@ -199,7 +207,9 @@ int int8_device(Int8Device* out) {
         for (const uint32_t f : {0u, kInt8YFp32, kInt8Bf16})
             for (const uint32_t acc : {0u, kInt8Accumulate})
                 if ((e = cudaFuncSetAttribute(pick_int8_tc(f | acc), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              kI8MaxSmem)) != cudaSuccess)
+                                              kI8MaxSmem)) != cudaSuccess ||
+                    (e = cudaFuncSetAttribute(pick_int8_pair(f | acc), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              kI8PairSmem)) != cudaSuccess)
                     return report_cuda_failure(e);
         const int st = device_error_word(dev, &d.err);
         if (st != FLUXBIN_OK) return st;
@@ -221,6 +231,50 @@ int encode_rows(CUtensorMap* map, const int8_t* base, int64_t rows, int64_t N, i
     return r == CUDA_SUCCESS ? FLUXBIN_OK : report_cuda_failure(cudaErrorInvalidValue);
 }
 
+// Tiles, split and ring of a call; returns the number of tiles.
+int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
+    Int8TcArgs& a = *out;
+    a.kblocks = (p.N + kI8K - 1) / kI8K;
+    // token tiles of equal size, a multiple of 16
+    a.tiles_t = (p.T + kI8MaxBn - 1) / kI8MaxBn;
+    a.bn = (((p.T + a.tiles_t - 1) / a.tiles_t) + 15) / 16 * 16;
+    const int64_t tiles = (int64_t)a.tiles_t * ((p.M + kI8Rows - 1) / kI8Rows);
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * d.sm_count && a.kblocks / (splits * 2) >= 2) splits *= 2;
+    a.splits = splits;
+    int smem = a.bn <= 64 ? 112 * 1024 : kI8MaxSmem;
+    const int stage = int8_stage_bytes(a.bn);
+    const int per_cta = a.kblocks / splits + 1;
+    a.stages = std::max(2, std::min(std::min(kI8MaxStages, per_cta), (smem - kI8RingOff) / stage));
+    if (splits > 1) a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
+    return tiles;
+}
+
+bool use_pairs(const Int8Args& p, const Int8Device& d) {
+    const int64_t tiles = ((int64_t)p.M + 255) / 256 * ((p.T + 255) / 256);
+    return p.T > 128 && tiles * 2 >= d.sm_count / 2;
+}
+
+int run_pairs(const Int8Args& p, const Int8Device& d, void* stream) {
+    Int8PairArgs a = {};
+    a.p = p;
+    a.kblocks = (p.N + kI8K - 1) / kI8K;
+    a.tiles_t = (p.T + kI8MaxBn - 1) / kI8MaxBn;
+    a.bn = (((p.T + a.tiles_t - 1) / a.tiles_t) + 31) / 32 * 32;
+    a.tiles_m = (p.M + 2 * kI8Rows - 1) / (2 * kI8Rows);
+    a.tiles = (int64_t)a.tiles_t * a.tiles_m;
+    a.test_stall = (p.flags & FLUXBIN_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
+    a.spin_limit = a.test_stall ? kI8TestSpinLimit : kI8SpinLimit;
+    a.err = d.err;
+    CUtensorMap mw, mx;
+    int st;
+    if ((st = encode_rows(&mw, p.w, p.M, p.N, p.ldw, kI8Rows)) != FLUXBIN_OK) return st;
+    if ((st = encode_rows(&mx, p.x, p.T, p.N, p.ldx, a.bn / 2)) != FLUXBIN_OK) return st;
+    const int64_t pairs = std::min<int64_t>(a.tiles, d.sm_count / 2);
+    return launch(pick_int8_pair(p.flags), dim3((unsigned)(2 * pairs)), dim3(kI8PairThreads), (size_t)kI8PairSmem, 1,
+                  stream, mw, mx, a);
+}
+
 int run_int8(const Int8Args& p, void* stream) {
     const bool acc = (p.flags & kInt8Accumulate) != 0;
     if (p.N == 0) {
@@ -233,21 +287,11 @@ int run_int8(const Int8Args& p, void* stream) {
     Int8Device d;
     int st = int8_device(&d);
     if (st != FLUXBIN_OK) return st;
+    if (use_pairs(p, d)) return run_pairs(p, d, stream);
     Int8TcArgs a = {};
     a.p = p;
-    a.kblocks = (p.N + kI8K - 1) / kI8K;
-    // token tiles of equal size, a multiple of 16
-    const int tiles_t = (p.T + kI8MaxBn - 1) / kI8MaxBn;
-    a.bn = (((p.T + tiles_t - 1) / tiles_t) + 15) / 16 * 16;
-    a.tiles_t = tiles_t;
-    const int64_t tiles = (int64_t)tiles_t * ((p.M + kI8Rows - 1) / kI8Rows);
-    int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= 2 * d.sm_count && a.kblocks / (splits * 2) >= 2) splits *= 2;
-    a.splits = splits;
-    const int stage = int8_stage_bytes(a.bn);
-    const int per_cta = a.kblocks / splits + 1;
-    a.stages = std::min(std::min(kI8MaxStages, per_cta), ((a.bn <= 64 ? 112 * 1024 : kI8MaxSmem) - kI8RingOff) / stage);
-    if (splits > 1) a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
+    const int64_t tiles = plan_int8(p, d, &a);
+    const int stage = int8_stage_bytes(a.bn), splits = a.splits;
     a.tmem_cols = 32;
     while ((int)a.tmem_cols < a.bn) a.tmem_cols *= 2;
     a.test_stall = (p.flags & FLUXBIN_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
@@ -334,6 +378,7 @@ int fluxbin_int8_linear(int32_t M, int32_t N, const int8_t* d_w, int64_t ldw, co
     a.N = N;
     a.T = T;
     a.flags = flags;
+    a.vec4 = ptr_aligned(d_y, 4 * ys) && ldy % 4 == 0;
     return run_int8(a, stream);
 }
 

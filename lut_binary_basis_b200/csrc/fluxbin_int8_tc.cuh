@@ -91,14 +91,54 @@ __device__ __forceinline__ void int8_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ int ld_dsmem(uint32_t addr, int rank) {
+__device__ __forceinline__ uint32_t dsmem_addr(uint32_t addr, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ int ld_dsmem(uint32_t addr) {
     int v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-        "ld.shared::cluster.b32 %0, [a];\n\t}"
-        : "=r"(v) : "r"(addr), "r"(rank) : "memory");
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ int4 ld_dsmem4(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Four consecutive channels m .. m+3 (fewer at the end of M) of token t.
+template <typename Y, bool ACC>
+__device__ __forceinline__ void int8_store4(const Int8Args& p, int64_t t, int m, float sx, const float (&sw)[4],
+                                            const int4& acc, bool ok) {
+    Y* y = static_cast<Y*>(p.y) + t * p.ldy + m;
+    const int n = p.M - m < 4 ? p.M - m : 4;
+    const int v4[4] = {acc.x, acc.y, acc.z, acc.w};
+    struct alignas(4 * sizeof(Y)) Quad { Y v[4]; } o;
+    const bool vec = p.vec4 && n == 4;
+    if (ACC) {
+        if (vec) {
+            o = *reinterpret_cast<const Quad*>(y);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o.v[i] = i < n ? y[i] : from_f32<Y>(0.f);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = int8_value(v4[i], sx, sw[i]);
+        if (!ok) v = __int_as_float(0x7fc00000);
+        if (ACC) v += to_f32(o.v[i]);
+        o.v[i] = from_f32<Y>(v);
+    }
+    if (vec) {
+        *reinterpret_cast<Quad*>(y) = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) y[i] = o.v[i];
+    }
 }
 
 // Writes 16 tokens t0 .. t0+15 (fewer at the end of T) of channel m, every
@@ -261,18 +301,36 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
     }
     if (a.splits > 1) {
         int8_cluster_sync();
-        // this CTA's share of the tile's tokens, added over the cluster
+        // this CTA's share of the tile's (token, four channels) items, added
+        // over the cluster
         bool all_ok = true;
-        for (int r = 0; r < a.splits; ++r) all_ok = all_ok && ld_dsmem(sb + kFailed, r) == 0;
-        const float sw = m < p.M ? p.sw[m] : 0.f;
-        const int groups = a.bn / 16, g0 = groups * rank / a.splits, g1 = groups * (rank + 1) / a.splits;
-        for (int c = 16 * g0; c < 16 * g1 && t0 + c < p.T; c += 16) {
-            int v[16] = {};
-            for (int r = 0; r < a.splits; ++r) {
+        for (int r = 0; r < a.splits; ++r) all_ok = all_ok && ld_dsmem(dsmem_addr(sb + kFailed, r)) == 0;
+        const int nt = (int)(p.T - t0 < a.bn ? p.T - t0 : a.bn);
+        const int items = nt * (kI8Rows / 4);
+        const int i0 = items * rank / a.splits, i1 = items * (rank + 1) / a.splits;
+        uint32_t peer[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] += ld_dsmem(red + (uint32_t)(((c + j) * kI8Rows + row) * 4), r);
-            }
-            if (m < p.M) int8_store16<Y, ACC>(p, t0 + c, m, sw, v, all_ok);
+        for (int r = 0; r < 8; ++r) peer[r] = dsmem_addr(red, r < a.splits ? r : 0);
+        for (int i = i0 + tid; i < i1; i += 128) {
+            const int c = i / (kI8Rows / 4), mq = 4 * (i % (kI8Rows / 4)), mg = tile_m * kI8Rows + mq;
+            int4 part[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < a.splits) part[r] = ld_dsmem4(peer[r] + (uint32_t)((c * kI8Rows + mq) * 4));
+            float sw4[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sw4[j] = mg + j < p.M ? __ldg(p.sw + mg + j) : 0.f;
+            const float sxv = __ldg(p.sx + t0 + c);
+            int4 v = part[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < a.splits) {
+                    v.x += part[r].x;
+                    v.y += part[r].y;
+                    v.z += part[r].z;
+                    v.w += part[r].w;
+                }
+            if (mg < p.M) int8_store4<Y, ACC>(p, t0 + c, mg, sxv, sw4, v, all_ok);
         }
         int8_cluster_sync();                     // the others have read this CTA's sums
     }

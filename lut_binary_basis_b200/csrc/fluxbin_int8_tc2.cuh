@@ -1,0 +1,259 @@
+// The 8-bit integer product for many tokens (sm_100a): pairs of CTAs.
+//
+// A pair owns a tile of 256 channels by `bn` tokens (a multiple of 32 up to
+// 256): one tcgen05.mma (cta_group::2) reads 128 channels from each CTA's
+// shared memory and half of the tokens from each, so that a CTA loads
+// 128 + bn/2 rows per stage where a lone CTA would load 128 + bn for the same
+// work.  That is what a product of this size needs: at the integer rate of
+// the tensor cores a lone 128 x 256 tile asks for 96 bytes per clock and SM
+// from L2, more than one SM takes in; the pair's asks for 64.
+//
+// The grid is persistent (one pair per two SMs) and each CTA holds two
+// accumulators in tensor memory: four warps empty one into y while the matrix
+// instructions of the next tile run into the other.
+//
+// Roles per CTA: warp 0 copies (TMA, both CTAs signal the leader's full
+// barriers), warp 1 of the leader issues the matrix instructions and commits
+// them to both CTAs' empty barriers, warps 2-5 write the outputs (channels lie
+// along the lanes: a warp stores 32 consecutive channels of a token).
+// Tiles run token tile by token tile within groups of 8 token tiles, so that
+// the pairs at work share their weights and a group's tokens through L2.
+//
+// A pair's CTAs wait for each other while they hold tensor memory, so no two
+// kernels that do may share an SM halfway: the ring takes more than half of an
+// SM's shared memory.
+#pragma once
+
+#include "fluxbin_int8_tc.cuh"
+
+namespace fluxbin {
+
+constexpr int kI8PairThreads = 192;
+constexpr int kI8PairStages = 6;
+constexpr int kI8PairGroup = 8;          // token tiles that share a pass over the weights
+
+struct Int8PairArgs {
+    Int8Args p;
+    int32_t bn, kblocks, tiles_t, tiles_m;
+    int64_t tiles;
+    uint32_t spin_limit;
+    int32_t test_stall;
+    unsigned int* err;
+};
+
+__host__ __device__ constexpr int int8_pair_stage_bytes(int bn) { return kI8Rows * kI8K + (bn / 2) * kI8K; }
+// Always sized for the widest tile: more than half of an SM's shared memory.
+constexpr int kI8PairSmem = kI8RingOff + kI8PairStages * int8_pair_stage_bytes(kI8MaxBn);
+
+__device__ __forceinline__ void int8_pair_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+}
+// A copy into this CTA's shared memory that signals a barrier of the pair.
+__device__ __forceinline__ void int8_pair_tma(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// Arrives on the same barrier of both CTAs once this thread's matrix instructions have finished.
+__device__ __forceinline__ void int8_pair_commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .b16 m;\n\t"
+        "mov.b16 m, 3;\n\t"
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+        ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void int8_remote_arrive(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void int8_ld32(uint32_t taddr, int (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+
+struct Int8PairTile {
+    int tm, tt;
+};
+__device__ __forceinline__ Int8PairTile int8_pair_tile(const Int8PairArgs& a, int64_t i) {
+    const int64_t per_group = (int64_t)kI8PairGroup * a.tiles_m;
+    const int g = (int)(i / per_group);
+    const int64_t r = i % per_group;
+    const int first = g * kI8PairGroup;
+    const int n = a.tiles_t - first < kI8PairGroup ? a.tiles_t - first : kI8PairGroup;
+    return Int8PairTile{(int)(r / n), first + (int)(r % n)};
+}
+
+template <typename Y, bool ACC>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
+    fluxbin_int8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                             const __grid_constant__ Int8PairArgs a) {
+    const Int8Args& p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sb = smem_base();
+    // barriers: full and empty per stage, accumulator full and empty (2), done
+    const uint32_t full0 = sb, empty0 = sb + 64, acc_full0 = sb + 128, acc_empty0 = sb + 144, done = sb + 160;
+    constexpr uint32_t kSlot = 168, kDrained = 172;
+    const uint32_t ring = sb + kI8RingOff;
+    const uint32_t stage_bytes = (uint32_t)int8_pair_stage_bytes(a.bn);
+    const int rank = (int)(blockIdx.x & 1);
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSlot), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int s = 0; s < kI8PairStages; ++s) {
+            tc_mbar_init(full0 + 8 * s, 1);
+            tc_mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc_mbar_init(acc_full0 + 8 * b, 1);
+            tc_mbar_init(acc_empty0 + 8 * b, 8);   // four warps of each CTA
+        }
+        tc_mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    int8_cluster_sync();                           // the other CTA's barriers exist
+    tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t tmem = smem_at<const uint32_t>(kSlot);
+    const bool aligned = (sb & 1023u) == 0;        // both CTAs have the same base
+    bool ok = aligned;
+
+    if (warp == 0) {
+        if (lane == 0 && aligned) {
+            // ---- copies: this CTA's half of the channels and of the tokens ----
+            const bool early = (p.flags & kInt8Early) != 0;
+            const int half = a.bn / 2;
+            int pre = 0;                           // stages whose weights were requested early
+            if (early && !a.test_stall && first < a.tiles) {
+                const Int8PairTile t = int8_pair_tile(a, first);
+                pre = a.kblocks < kI8PairStages ? a.kblocks : kI8PairStages;
+                for (int s = 0; s < pre; ++s) {
+                    if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
+                    int8_pair_tma(ring + s * stage_bytes, &map_w, s * kI8K, t.tm * 2 * kI8Rows + rank * kI8Rows,
+                                  dsmem_addr(full0 + 8 * s, 0));
+                }
+            }
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int s = 0;
+            uint32_t round = 0;                    // times the ring has been filled before
+            for (int64_t i = first; i < a.tiles && ok && !a.test_stall; i += step) {
+                const Int8PairTile t = int8_pair_tile(a, i);
+                for (int k = 0; k < a.kblocks; ++k) {
+                    const uint32_t bar = dsmem_addr(full0 + 8 * s, 0), dst = ring + s * stage_bytes;
+                    if (round > 0 && !(ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit))) break;
+                    if (pre > 0) {
+                        --pre;
+                    } else {
+                        if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
+                        int8_pair_tma(dst, &map_w, k * kI8K, t.tm * 2 * kI8Rows + rank * kI8Rows, bar);
+                    }
+                    int8_pair_tma(dst + kI8Rows * kI8K, &map_x, k * kI8K, t.tt * a.bn + rank * half, bar);
+                    if (++s == kI8PairStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            if (!ok) {
+                atomicOr(a.err, 1u);
+                // the copies in flight land within microseconds; the leader's
+                // barriers cannot be waited for from the other CTA, so a copier
+                // that gave up stays for a millisecond
+                for (int w = 0; w < 1000; ++w) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0 && aligned) {
+            // ---- matrix instructions, for both CTAs ----
+            const uint32_t idesc = int8_idesc(2 * kI8Rows, a.bn);
+            int s = 0;
+            uint32_t round = 0;
+            int64_t n = 0;                         // tiles so far
+            for (int64_t i = first; i < a.tiles && ok; i += step, ++n) {
+                const int b = (int)(n & 1);
+                if (n >= 2) ok = tc_mbar_wait(acc_empty0 + 8 * b, (uint32_t)((n >> 1) - 1) & 1u, a.spin_limit);
+                tc_fence_after();
+                for (int k = 0; k < a.kblocks && ok; ++k) {
+                    if (!(ok = tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit))) break;
+                    tc_fence_after();
+                    const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
+                    const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        int8_pair_mma(tmem + (uint32_t)(b * kI8MaxBn), da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
+                    int8_pair_commit(empty0 + 8 * s);
+                    if (++s == kI8PairStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+                if (ok) int8_pair_commit(acc_full0 + 8 * b);
+            }
+            int8_pair_commit(done);                // every instruction issued above has finished
+            if (!ok) atomicOr(a.err, 1u);
+        }
+    } else {
+        // ---- outputs ----
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int quarter = warp & 3;              // the lanes of tensor memory that this warp reaches
+        int64_t n = 0;
+        for (int64_t i = first; i < a.tiles; i += step, ++n) {
+            const Int8PairTile t = int8_pair_tile(a, i);
+            const int b = (int)(n & 1);
+            if (ok) ok = tc_mbar_wait(acc_full0 + 8 * b, (uint32_t)(n >> 1) & 1u, a.spin_limit);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            const int m = (t.tm * 2 + rank) * kI8Rows + quarter * 32 + lane;
+            const int64_t t0 = (int64_t)t.tt * a.bn;
+            const float sw = m < p.M ? __ldg(p.sw + m) : 0.f;
+            const uint32_t acc = tmem + (uint32_t)(b * kI8MaxBn) + ((uint32_t)(quarter * 32) << 16);
+            for (int c = 0; c < a.bn; c += 32) {
+                int v[32];
+                int8_ld32(acc + (uint32_t)c, v);
+                tc_wait_ld();
+                if (c + 32 >= a.bn) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) int8_remote_arrive(dsmem_addr(acc_empty0 + 8 * b, 0));
+                }
+                if (m < p.M) {
+                    if (t0 + c < p.T) int8_store16<Y, ACC>(p, t0 + c, m, sw, reinterpret_cast<const int(&)[16]>(v[0]), ok);
+                    if (t0 + c + 16 < p.T)
+                        int8_store16<Y, ACC>(p, t0 + c + 16, m, sw, reinterpret_cast<const int(&)[16]>(v[16]), ok);
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(a.err, 1u);
+    }
+    __syncwarp();
+    const bool drained = aligned ? tc_mbar_wait(done, 0u, kI8SpinLimit) : true;
+    if (!drained && tid == 0) atomicOr(a.err, 2u);
+    tc_fence_before();
+    // the release takes both CTAs: each knows whether the other's wait went well
+    const int all_drained = __syncthreads_and(drained);
+    if (tid == 0) smem_at<int>(kDrained) = all_drained;
+    int8_cluster_sync();
+    const bool release = all_drained && ld_dsmem(dsmem_addr(sb + kDrained, rank ^ 1)) != 0;
+    int8_cluster_sync();
+    if (warp == 1 && release) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+}  // namespace fluxbin
