@@ -172,7 +172,7 @@ Int8TcFn pick_int8_tc(uint32_t flags) {
     const bool acc = (flags & kInt8Accumulate) != 0;
     return (flags & kInt8YFp32) ? pick_tc<float>(acc) : (flags & kInt8Bf16) ? pick_tc<__nv_bfloat16>(acc) : pick_tc<__half>(acc);
 }
-using Int8PairFn = void (*)(CUtensorMap, CUtensorMap, Int8PairArgs);
+using Int8PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Int8PairArgs);
 template <typename Y>
 Int8PairFn pick_pair(bool acc) { return acc ? &fluxbin_int8_pair_kernel<Y, true> : &fluxbin_int8_pair_kernel<Y, false>; }
 Int8PairFn pick_int8_pair(uint32_t flags) {
@@ -231,6 +231,18 @@ int encode_rows(CUtensorMap* map, const int8_t* base, int64_t rows, int64_t N, i
     return r == CUDA_SUCCESS ? FLUXBIN_OK : report_cuda_failure(cudaErrorInvalidValue);
 }
 
+// y as a tensor map: boxes of 128 channels by the tokens of one staging buffer.
+int encode_y(CUtensorMap* map, const Int8Args& p, int size) {
+    const cuuint64_t dims[2] = {(cuuint64_t)p.M, (cuuint64_t)p.T};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.ldy * (cuuint64_t)size};
+    const cuuint32_t boxes[2] = {(cuuint32_t)kI8Rows, (cuuint32_t)kI8PairChunk};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = g_encode(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.y,
+                                dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FLUXBIN_OK : report_cuda_failure(cudaErrorInvalidValue);
+}
+
 // Tiles, split and ring of a call; returns the number of tiles.
 int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
     Int8TcArgs& a = *out;
@@ -270,9 +282,15 @@ int run_pairs(const Int8Args& p, const Int8Device& d, void* stream) {
     int st;
     if ((st = encode_rows(&mw, p.w, p.M, p.N, p.ldw, kI8Rows)) != FLUXBIN_OK) return st;
     if ((st = encode_rows(&mx, p.x, p.T, p.N, p.ldx, a.bn / 2)) != FLUXBIN_OK) return st;
+    // y by TMA where its rows allow: 16-byte aligned rows
+    const int ys = (p.flags & kInt8YFp32) ? 4 : 2;
+    if (ptr_aligned(p.y, 16) && (p.ldy * ys) % 16 == 0 && p.ldy * ys < ((int64_t)1 << 40))
+        a.bulk = ((int64_t)p.M * ys) % 16 == 0 ? 2 : 1;
+    CUtensorMap my = mx;
+    if (a.bulk && (st = encode_y(&my, p, ys)) != FLUXBIN_OK) return st;
     const int64_t pairs = std::min<int64_t>(a.tiles, d.sm_count / 2);
     return launch(pick_int8_pair(p.flags), dim3((unsigned)(2 * pairs)), dim3(kI8PairThreads), (size_t)kI8PairSmem, 1,
-                  stream, mw, mx, a);
+                  stream, mw, mx, my, a);
 }
 
 int run_int8(const Int8Args& p, void* stream) {

@@ -38,12 +38,17 @@ struct Int8PairArgs {
     int64_t tiles;
     uint32_t spin_limit;
     int32_t test_stall;
+    int32_t bulk;         // y's rows can be written (and read) by TMA: 1 whole tiles, 2 a ragged last tile too
     unsigned int* err;
 };
 
 __host__ __device__ constexpr int int8_pair_stage_bytes(int bn) { return kI8Rows * kI8K + (bn / 2) * kI8K; }
-// Always sized for the widest tile: more than half of an SM's shared memory.
-constexpr int kI8PairSmem = kI8RingOff + kI8PairStages * int8_pair_stage_bytes(kI8MaxBn);
+// Always sized for the widest tile and y: all of an SM's shared memory.
+constexpr int kI8PairChunk = 32;         // tokens staged at a time
+constexpr int kI8PairOutOff = kI8RingOff + kI8PairStages * int8_pair_stage_bytes(kI8MaxBn);
+constexpr int kI8PairOutBytes = kI8PairChunk * kI8Rows * 4;        // one of two staging buffers
+constexpr int kI8PairSxOff = kI8PairOutOff + 2 * kI8PairOutBytes;  // [2][256] token scales
+constexpr int kI8PairSmem = kI8PairSxOff + 2 * kI8MaxBn * 4;
 
 __device__ __forceinline__ void int8_pair_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
     asm volatile(
@@ -80,6 +85,18 @@ __device__ __forceinline__ void int8_ld32(uint32_t taddr, int (&v)[32]) {
         : "r"(taddr));
 }
 
+// The four output warps.
+__device__ __forceinline__ void int8_out_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Requests chunk q of a tile's y (accumulation) into its staging buffer.
+__device__ __forceinline__ void int8_pair_load_y(const CUtensorMap& map_y, uint32_t sb, int m0, int64_t t0, int q,
+                                                 uint32_t y_full0, int size) {
+    const int buf = q & 1;
+    int8_expect(y_full0 + 8 * buf, (uint32_t)(kI8PairChunk * kI8Rows * size));
+    int8_tma(sb + (uint32_t)(kI8PairOutOff + buf * kI8PairOutBytes), &map_y, m0, (int)t0 + q * kI8PairChunk,
+             y_full0 + 8 * buf);
+}
+
 struct Int8PairTile {
     int tm, tt;
 };
@@ -95,13 +112,14 @@ __device__ __forceinline__ Int8PairTile int8_pair_tile(const Int8PairArgs& a, in
 template <typename Y, bool ACC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
     fluxbin_int8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                             const __grid_constant__ Int8PairArgs a) {
+                             const __grid_constant__ CUtensorMap map_y, const __grid_constant__ Int8PairArgs a) {
     const Int8Args& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sb = smem_base();
     // barriers: full and empty per stage, accumulator full and empty (2), done
-    const uint32_t full0 = sb, empty0 = sb + 64, acc_full0 = sb + 128, acc_empty0 = sb + 144, done = sb + 160;
-    constexpr uint32_t kSlot = 168, kDrained = 172;
+    const uint32_t full0 = sb, empty0 = sb + 64, acc_full0 = sb + 128, acc_empty0 = sb + 144, done = sb + 160,
+                   y_full0 = sb + 168;
+    constexpr uint32_t kSlot = 184, kDrained = 188;
     const uint32_t ring = sb + kI8RingOff;
     const uint32_t stage_bytes = (uint32_t)int8_pair_stage_bytes(a.bn);
     const int rank = (int)(blockIdx.x & 1);
@@ -120,6 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
         for (int b = 0; b < 2; ++b) {
             tc_mbar_init(acc_full0 + 8 * b, 1);
             tc_mbar_init(acc_empty0 + 8 * b, 8);   // four warps of each CTA
+            tc_mbar_init(y_full0 + 8 * b, 1);
         }
         tc_mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -211,33 +230,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
         // ---- outputs ----
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const int quarter = warp & 3;              // the lanes of tensor memory that this warp reaches
+        const int e = tid - 64, row = quarter * 32 + lane;
+        const int chunks = a.bn / kI8PairChunk;
+        uint32_t y_parity = 0u;                    // of the loads of y into each staging buffer (one bit each)
         int64_t n = 0;
         for (int64_t i = first; i < a.tiles; i += step, ++n) {
             const Int8PairTile t = int8_pair_tile(a, i);
             const int b = (int)(n & 1);
+            const int m0 = (t.tm * 2 + rank) * kI8Rows, m = m0 + row;
+            const int64_t t0 = (int64_t)t.tt * a.bn;
+            // the tile's scales, requested before the accumulators are ready
+            const float sw = m < p.M ? __ldg(p.sw + m) : 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = h * 128 + e;
+                smem_at<float>(kI8PairSxOff + (b * kI8MaxBn + c) * 4) = c < a.bn && t0 + c < p.T ? __ldg(p.sx + t0 + c) : 0.f;
+            }
+            // TMA writes whole 16-byte pieces: a ragged last tile only where
+            // M ends on one
+            const bool bulk = a.bulk > (m0 + kI8Rows <= p.M ? 0 : 1);
+            if (ACC && bulk && e == 0) {
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                int8_pair_load_y(map_y, sb, m0, t0, 0, y_full0, (int)sizeof(Y));
+            }
             if (ok) ok = tc_mbar_wait(acc_full0 + 8 * b, (uint32_t)(n >> 1) & 1u, a.spin_limit);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            const int m = (t.tm * 2 + rank) * kI8Rows + quarter * 32 + lane;
-            const int64_t t0 = (int64_t)t.tt * a.bn;
-            const float sw = m < p.M ? __ldg(p.sw + m) : 0.f;
+            int8_out_sync();                       // the token scales are in place
             const uint32_t acc = tmem + (uint32_t)(b * kI8MaxBn) + ((uint32_t)(quarter * 32) << 16);
-            for (int c = 0; c < a.bn; c += 32) {
+            for (int q = 0; q < chunks; ++q) {
+                const int buf = q & 1, c = q * kI8PairChunk;
+                const uint32_t out = (uint32_t)(kI8PairOutOff + buf * kI8PairOutBytes);
                 int v[32];
                 int8_ld32(acc + (uint32_t)c, v);
+                if (bulk) {
+                    // the staging buffer is free once the copy out of it two
+                    // chunks ago has been read; with accumulation the next
+                    // chunk's y is requested a chunk ahead
+                    if (e == 0) {
+                        if (ACC) {
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                            if (q + 1 < chunks) int8_pair_load_y(map_y, sb, m0, t0, q + 1, y_full0, (int)sizeof(Y));
+                        } else {
+                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        }
+                    }
+                    if (!ACC) int8_out_sync();
+                }
+                float f[32];
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 s4 = smem_at<const float4>(kI8PairSxOff + (b * kI8MaxBn + c + j) * 4);
+                    f[j] = s4.x;
+                    f[j + 1] = s4.y;
+                    f[j + 2] = s4.z;
+                    f[j + 3] = s4.w;
+                }
                 tc_wait_ld();
-                if (c + 32 >= a.bn) {
+                if (q == chunks - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) int8_remote_arrive(dsmem_addr(acc_empty0 + 8 * b, 0));
                 }
-                if (m < p.M) {
-                    if (t0 + c < p.T) int8_store16<Y, ACC>(p, t0 + c, m, sw, reinterpret_cast<const int(&)[16]>(v[0]), ok);
-                    if (t0 + c + 16 < p.T)
-                        int8_store16<Y, ACC>(p, t0 + c + 16, m, sw, reinterpret_cast<const int(&)[16]>(v[16]), ok);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    f[j] = int8_value(v[j], f[j], sw);
+                    if (!ok) f[j] = __int_as_float(0x7fc00000);
+                }
+                if (bulk) {
+                    if (ACC) {
+                        ok = tc_mbar_wait(y_full0 + 8 * buf, (y_parity >> buf) & 1u, kI8SpinLimit) && ok;
+                        y_parity ^= 1u << buf;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        Y& o = smem_at<Y>(out + (uint32_t)((j * kI8Rows + row) * sizeof(Y)));
+                        o = from_f32<Y>(ACC ? to_f32(o) + f[j] : f[j]);
+                    }
+                    fence_async_smem();
+                    int8_out_sync();
+                    if (e == 0 && t0 + c < p.T && m0 < p.M) {
+                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                                     ::"l"(&map_y), "r"(m0), "r"((int)(t0 + c)), "r"(sb + out) : "memory");
+                    }
+                    if (e == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                } else if (m < p.M) {
+                    Y* y = static_cast<Y*>(p.y) + (t0 + c) * p.ldy + m;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (t0 + c + j < p.T) *y = from_f32<Y>(ACC ? to_f32(*y) + f[j] : f[j]);
+                        y += p.ldy;
+                    }
                 }
             }
         }
+        if (a.bulk && e == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok && lane == 0) atomicOr(a.err, 1u);
     }
     __syncwarp();

@@ -170,6 +170,29 @@ def test_unaligned_y():
             assert bool((buf[:, :1] == 3).all()) and bool((buf[:, 302:] == 3).all())
 
 
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("T,M,N", [(129, 9473, 130), (300, 5000, 400), (700, 3333, 256), (1025, 2600, 1000), (2500, 1100, 300)])
+@pytest.mark.parametrize("pad,first", [(0, 0), (8, 8), (3, 0), (8, 1)])
+def test_many_tiles(T, M, N, pad, first, kind):
+    """Enough tiles for several rounds of every CTA, several groups of token
+    tiles, ragged ends; y with rows that allow bulk copies and rows that do
+    not, stored and accumulated."""
+    layer, rows, want = problem(T, M, N, seed=10)
+    if kind == "fp16":
+        layer.scale.mul_(2.0 ** -4)
+        want = want * 2.0 ** -4
+    ld = -(-M // 8) * 8 + pad + first
+    buf = torch.full((T + 1, ld), 5.0, dtype=DT[kind], device="cuda")
+    y = buf[:T, first:first + M]
+    layer.linear(rows, y)
+    check(y, want, kind)
+    y.copy_(torch.randn(T, M, device="cuda"))
+    y0 = y.float().cpu().numpy().astype(np.float64)
+    layer.linear(rows, y, fluxbin.FLAG_ACCUMULATE)
+    check(y, want, kind, y0)
+    assert bool((buf[T] == 5).all()) and bool((buf[:T, :first] == 5).all()) and bool((buf[:T, first + M:] == 5).all())
+
+
 def test_repeated_calls_and_streams():
     """Calls that overlap on two streams, with no order between them."""
     layer, rows, want = problem(24, 1500, 2000, seed=5)
