@@ -17,7 +17,7 @@
 // CTA releases its tensor memory before it waits for the others (none holds
 // tensor memory while it waits for one that may be waiting for some).
 //
-// Roles: thread 0 of warp 0 issues the copies, thread 0 of warp 1 the matrix
+// Roles: one thread of warp 0 issues the copies, one of warp 1 the matrix
 // instructions; a ring of stages with full and empty mbarriers lies between
 // them.  All four warps then empty the accumulators.  Every wait is bounded:
 // one that gives up sets bit 0 of the device error word, and the CTA's sums
@@ -59,6 +59,20 @@ __host__ __device__ constexpr int int8_stage_bytes(int bn) { return kI8Rows * kI
 // accumulator, signed A and B, both K-major.
 __device__ __forceinline__ uint32_t int8_idesc(int m, int n) {
     return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// One thread of a converged warp, the same one every time.  A branch on it,
+// unlike one on the lane number, is known to be taken by a single thread: the
+// matrix instructions' descriptors then stay in uniform registers (the pair
+// kernel at 4096 x 8192 x 8192: 305,000 -> 263,000 cycles).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void int8_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
@@ -235,26 +249,30 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
         // copies in flight land before the CTA ends: the last fill of every stage
         for (int k = i > a.stages ? i - a.stages : 0; k < i; ++k)
             (void)tc_mbar_wait(full0 + 8 * (k % a.stages), (uint32_t)(k / a.stages) & 1u, kI8SpinLimit);
-    } else if (warp == 1 && lane == 0 && aligned) {
+    } else if (warp == 1 && aligned) {
         // ---- matrix instructions ----
         const uint32_t idesc = int8_idesc(kI8Rows, a.bn);
         bool ok = true;
-        int i = 0;
-        for (; i < nk && ok; ++i) {
+        for (int i = 0; i < nk; ++i) {
             const int s = i % a.stages;
             ok = tc_mbar_wait(full0 + 8 * s, (uint32_t)(i / a.stages) & 1u, a.spin_limit);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
-            const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
+            if (elect_one()) {
+                const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
+                const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) int8_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
-            tc_commit(empty0 + 8 * s);
+                for (int k = 0; k < 4; ++k) int8_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
+                tc_commit(empty0 + 8 * s);
+            }
+            __syncwarp();
         }
-        tc_commit(done);   // every instruction issued above has finished (at once when there is none)
-        if (!ok) {
-            atomicOr(a.err, 1u);
-            smem_at<uint32_t>(kFailed) = 1u;
+        if (elect_one()) {
+            tc_commit(done);   // every instruction issued above has finished (at once when there is none)
+            if (!ok) {
+                atomicOr(a.err, 1u);
+                smem_at<uint32_t>(kFailed) = 1u;
+            }
         }
     }
     __syncwarp();

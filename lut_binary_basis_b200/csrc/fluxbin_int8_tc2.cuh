@@ -197,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0 && aligned) {
+        if (rank == 0 && aligned) {
             // ---- matrix instructions, for both CTAs ----
             const uint32_t idesc = int8_idesc(2 * kI8Rows, a.bn);
             int s = 0;
@@ -207,24 +207,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 const int b = (int)(n & 1);
                 if (n >= 2) ok = tc_mbar_wait(acc_empty0 + 8 * b, (uint32_t)((n >> 1) - 1) & 1u, a.spin_limit);
                 tc_fence_after();
-                for (int k = 0; k < a.kblocks && ok; ++k) {
-                    if (!(ok = tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit))) break;
-                    tc_fence_after();
-                    const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
-                    const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
+                for (int k = 0; k < a.kblocks; ++k) {
+                    ok = ok && tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
+                        const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        int8_pair_mma(tmem + (uint32_t)(b * kI8MaxBn), da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
-                    int8_pair_commit(empty0 + 8 * s);
+                        for (int q = 0; q < 4; ++q)
+                            int8_pair_mma(tmem + (uint32_t)(b * kI8MaxBn), da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
+                        int8_pair_commit(empty0 + 8 * s);
+                    }
+                    __syncwarp();
                     if (++s == kI8PairStages) {
                         s = 0;
                         ++round;
                     }
                 }
-                if (ok) int8_pair_commit(acc_full0 + 8 * b);
+                if (ok && elect_one()) int8_pair_commit(acc_full0 + 8 * b);
+                __syncwarp();
             }
-            int8_pair_commit(done);                // every instruction issued above has finished
-            if (!ok) atomicOr(a.err, 1u);
+            if (elect_one()) {
+                int8_pair_commit(done);            // every instruction issued above has finished
+                if (!ok) atomicOr(a.err, 1u);
+            }
         }
     } else {
         // ---- outputs ----
