@@ -163,7 +163,7 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeFn g_encode = nullptr;
 
-using Int8TcFn = void (*)(CUtensorMap, CUtensorMap, Int8TcArgs);
+using Int8TcFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Int8TcArgs);
 using Int8EmptyFn = void (*)(Int8Args);
 
 template <typename Y>
@@ -231,11 +231,18 @@ int encode_rows(CUtensorMap* map, const int8_t* base, int64_t rows, int64_t N, i
     return r == CUDA_SUCCESS ? FLUXBIN_OK : report_cuda_failure(cudaErrorInvalidValue);
 }
 
-// y as a tensor map: boxes of 128 channels by the tokens of one staging buffer.
-int encode_y(CUtensorMap* map, const Int8Args& p, int size) {
+// Whether y's rows can be written by TMA (16-byte aligned, a pitch it can
+// hold): 1 for whole tiles, 2 for a ragged last tile too (it writes whole
+// 16-byte pieces); 0 otherwise.  If so, `map` receives y with boxes of 128
+// channels by `box` tokens.
+int encode_y(CUtensorMap* map, const Int8Args& p, int box, int32_t* bulk) {
+    const int size = (p.flags & kInt8YFp32) ? 4 : 2;
+    *bulk = 0;
+    if (!ptr_aligned(p.y, 16) || (p.ldy * size) % 16 || p.ldy * size >= ((int64_t)1 << 40)) return FLUXBIN_OK;
+    *bulk = ((int64_t)p.M * size) % 16 == 0 ? 2 : 1;
     const cuuint64_t dims[2] = {(cuuint64_t)p.M, (cuuint64_t)p.T};
     const cuuint64_t strides[1] = {(cuuint64_t)p.ldy * (cuuint64_t)size};
-    const cuuint32_t boxes[2] = {(cuuint32_t)kI8Rows, (cuuint32_t)kI8PairChunk};
+    const cuuint32_t boxes[2] = {(cuuint32_t)kI8Rows, (cuuint32_t)box};
     const cuuint32_t steps[2] = {1, 1};
     const CUresult r = g_encode(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.y,
                                 dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -244,36 +251,73 @@ int encode_y(CUtensorMap* map, const Int8Args& p, int size) {
 }
 
 // Tiles, split and ring of a call; returns the number of tiles.
+//
+// A tile's K is split until the CTAs fill one wave of the GPU, never more
+// (B200, us a call, a graph of calls on rotated weights; splits 1 / 3 / 4:
+// 16x11008x4096, 86 tiles on 296 slots 14.3 / 11.2 / 16.3 with the fourth in a
+// second wave).  Two CTAs per SM (112 KB each) as long as that leaves a ring of
+// three stages or more; wider tiles take the whole SM (128x4096x4096 10.8
+// against 11.4), unless its 148 slots would stay a quarter empty
+// (128x11008x4096, 86 tiles: 3 splits on two CTAs per SM 14.6, none on one
+// 16.2).  One CTA per SM is enough where a CTA's share is down to 8 stages
+// (1x4096x4096 with 4 splits 7.4, with 8 7.6; 1x4096x11008 12.8 and 11.7).
 int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
     Int8TcArgs& a = *out;
     a.kblocks = (p.N + kI8K - 1) / kI8K;
     // token tiles of equal size, a multiple of 16
-    a.tiles_t = (p.T + kI8MaxBn - 1) / kI8MaxBn;
-    a.bn = (((p.T + a.tiles_t - 1) / a.tiles_t) + 15) / 16 * 16;
-    const int64_t tiles = (int64_t)a.tiles_t * ((p.M + kI8Rows - 1) / kI8Rows);
-    int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= 2 * d.sm_count && a.kblocks / (splits * 2) >= 2) splits *= 2;
+    a.tiles_t = (int)(((int64_t)p.T + kI8MaxBn - 1) / kI8MaxBn);
+    a.bn = (int)((((int64_t)p.T + a.tiles_t - 1) / a.tiles_t) + 15) / 16 * 16;
+    const int64_t tiles = (int64_t)a.tiles_t * (((int64_t)p.M + kI8Rows - 1) / kI8Rows);
+    const int one = (int)std::min<int64_t>(kI8MaxSplits, d.sm_count / tiles);
+    const int two = (int)std::min<int64_t>(kI8MaxSplits, 2 * d.sm_count / tiles);
+    const bool whole = a.bn > 192 || (a.bn > 112 && one * tiles * 4 >= 3 * d.sm_count);
+    int splits = whole || (one >= 1 && a.kblocks <= 8 * one) ? one : two;
+    splits = std::max(1, std::min(splits, a.kblocks / 2));
     a.splits = splits;
-    int smem = a.bn <= 64 ? 112 * 1024 : kI8MaxSmem;
+    const int smem = whole ? kI8MaxSmem : 112 * 1024;
     const int stage = int8_stage_bytes(a.bn);
     const int per_cta = a.kblocks / splits + 1;
     a.stages = std::max(2, std::min(std::min(kI8MaxStages, per_cta), (smem - kI8RingOff) / stage));
-    if (splits > 1) a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
+    // the ring holds the tile's partial sums, or its y, at the end
+    a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
     return tiles;
 }
 
+// Token tile of the pair kernel, a multiple of 32: the one whose rounds of
+// the persistent grid cost least.  Below 256 tokens a round gets only a little
+// shorter, since the weights' copies bound it (one round at 4096x4096, 128 /
+// 192 / 256 tokens a tile: 13.6 / 14.6 / 16.0 us).  512x4096x4096: 128 tokens,
+// 64 tiles in one round, 14.7 us; 256 tokens 16.2.  512x11008x4096, two rounds
+// either way: 192 tokens 25.1, 256 tokens 26.0.
+int pair_tile(const Int8Args& p, const Int8Device& d) {
+    const int64_t tiles_m = ((int64_t)p.M + 2 * kI8Rows - 1) / (2 * kI8Rows), pairs = d.sm_count / 2;
+    int best = kI8MaxBn;
+    int64_t cost = INT64_MAX;
+    for (int bn = kI8MaxBn; bn >= 96; bn -= 32) {
+        const int64_t r = (tiles_m * (((int64_t)p.T + bn - 1) / bn) + pairs - 1) / pairs;
+        if (r * (384 + bn / 2) < cost) {
+            cost = r * (384 + bn / 2);
+            best = bn;
+        }
+    }
+    return best;
+}
+
+// Pairs from 257 tokens on, where their tiles fill half of the GPU
+// (333x4096x11008: 64 tiles of the split kernel 24.1 us, 64 of pairs 28.0;
+// 512x4096x4096 16.0 and 14.7; 256x11008x4096 17.4 and 18.2).
 bool use_pairs(const Int8Args& p, const Int8Device& d) {
-    const int64_t tiles = ((int64_t)p.M + 255) / 256 * ((p.T + 255) / 256);
-    return p.T > 128 && tiles * 2 >= d.sm_count / 2;
+    const int64_t tiles = ((int64_t)p.M + 255) / 256 * (((int64_t)p.T + 127) / 128);
+    return p.T > kI8MaxBn && tiles * 4 >= 3 * (d.sm_count / 2);
 }
 
 int run_pairs(const Int8Args& p, const Int8Device& d, void* stream) {
     Int8PairArgs a = {};
     a.p = p;
     a.kblocks = (p.N + kI8K - 1) / kI8K;
-    a.tiles_t = (p.T + kI8MaxBn - 1) / kI8MaxBn;
-    a.bn = (((p.T + a.tiles_t - 1) / a.tiles_t) + 31) / 32 * 32;
-    a.tiles_m = (p.M + 2 * kI8Rows - 1) / (2 * kI8Rows);
+    a.bn = pair_tile(p, d);
+    a.tiles_t = (int)(((int64_t)p.T + a.bn - 1) / a.bn);
+    a.tiles_m = (int)(((int64_t)p.M + 2 * kI8Rows - 1) / (2 * kI8Rows));
     a.tiles = (int64_t)a.tiles_t * a.tiles_m;
     a.test_stall = (p.flags & FLUXBIN_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
     a.spin_limit = a.test_stall ? kI8TestSpinLimit : kI8SpinLimit;
@@ -282,12 +326,8 @@ int run_pairs(const Int8Args& p, const Int8Device& d, void* stream) {
     int st;
     if ((st = encode_rows(&mw, p.w, p.M, p.N, p.ldw, kI8Rows)) != FLUXBIN_OK) return st;
     if ((st = encode_rows(&mx, p.x, p.T, p.N, p.ldx, a.bn / 2)) != FLUXBIN_OK) return st;
-    // y by TMA where its rows allow: 16-byte aligned rows
-    const int ys = (p.flags & kInt8YFp32) ? 4 : 2;
-    if (ptr_aligned(p.y, 16) && (p.ldy * ys) % 16 == 0 && p.ldy * ys < ((int64_t)1 << 40))
-        a.bulk = ((int64_t)p.M * ys) % 16 == 0 ? 2 : 1;
     CUtensorMap my = mx;
-    if (a.bulk && (st = encode_y(&my, p, ys)) != FLUXBIN_OK) return st;
+    if ((st = encode_y(&my, p, kI8PairChunk, &a.bulk)) != FLUXBIN_OK) return st;
     const int64_t pairs = std::min<int64_t>(a.tiles, d.sm_count / 2);
     return launch(pick_int8_pair(p.flags), dim3((unsigned)(2 * pairs)), dim3(kI8PairThreads), (size_t)kI8PairSmem, 1,
                   stream, mw, mx, my, a);
@@ -319,8 +359,10 @@ int run_int8(const Int8Args& p, void* stream) {
     CUtensorMap mw, mx;
     if ((st = encode_rows(&mw, p.w, p.M, p.N, p.ldw, kI8Rows)) != FLUXBIN_OK) return st;
     if ((st = encode_rows(&mx, p.x, p.T, p.N, p.ldx, a.bn)) != FLUXBIN_OK) return st;
-    return launch(pick_int8_tc(p.flags), dim3((unsigned)(tiles * splits)), dim3(128),
-                  (size_t)(kI8RingOff + a.stages * stage), splits, stream, mw, mx, a);
+    CUtensorMap my = mx;
+    if (splits == 1 && !acc && (st = encode_y(&my, p, kI8OutBox, &a.bulk)) != FLUXBIN_OK) return st;
+    return launch(pick_int8_tc(p.flags), dim3((unsigned)(tiles * splits)), dim3(kI8Threads),
+                  (size_t)(kI8RingOff + a.stages * stage), splits, stream, mw, mx, my, a);
 }
 
 }  // namespace

@@ -19,7 +19,7 @@
 //
 // Roles: one thread of warp 0 issues the copies, one of warp 1 the matrix
 // instructions; a ring of stages with full and empty mbarriers lies between
-// them.  All four warps then empty the accumulators.  Every wait is bounded:
+// them.  All eight warps then empty the accumulators.  Every wait is bounded:
 // one that gives up sets bit 0 of the device error word, and the CTA's sums
 // are replaced by NaN outputs.
 #pragma once
@@ -35,6 +35,7 @@ constexpr int kI8Rows = 128;                     // channels of a tile
 constexpr int kI8K = 128;                        // codes of K a stage (one swizzle row)
 constexpr int kI8MaxBn = 256;
 constexpr int kI8MaxStages = 12;
+constexpr int kI8MaxSplits = 8;                  // a portable cluster
 constexpr uint32_t kI8SpinLimit = 1u << 22;      // polls (each may suspend for microseconds) before a wait fails
 constexpr uint32_t kI8TestSpinLimit = 64u;
 
@@ -48,11 +49,15 @@ struct Int8TcArgs {
     uint32_t tmem_cols;
     uint32_t spin_limit;
     int32_t test_stall;   // test hook: no copy is issued
+    int32_t bulk;         // y's rows can be written by TMA: 1 whole tiles, 2 a ragged last tile too
     unsigned int* err;
 };
 
-// Byte offset of the ring behind the barriers (1024-byte atoms).
-constexpr int kI8RingOff = 1024;
+constexpr int kI8Threads = 256;
+constexpr int kI8OutBox = 16;                    // tokens of y written by one bulk copy
+// Token scales behind the barriers, then the ring (1024-byte atoms).
+constexpr int kI8SxOff = 1024;
+constexpr int kI8RingOff = 2048;
 __host__ __device__ constexpr int int8_stage_bytes(int bn) { return kI8Rows * kI8K + bn * kI8K; }
 
 // Instruction descriptor of the 8-bit integer kind: 32-bit integer
@@ -155,32 +160,14 @@ __device__ __forceinline__ void int8_store4(const Int8Args& p, int64_t t, int m,
     }
 }
 
-// Writes 16 tokens t0 .. t0+15 (fewer at the end of T) of channel m, every
-// load before the first store.
-template <typename Y, bool ACC>
-__device__ __forceinline__ void int8_store16(const Int8Args& p, int64_t t0, int m, float sw, const int (&acc)[16],
-                                             bool ok) {
-    Y* y = static_cast<Y*>(p.y) + t0 * p.ldy + m;
-    const int n = (int)(p.T - t0 < 16 ? p.T - t0 : 16);
-    float s[16], old[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        s[j] = j < n ? __ldg(p.sx + t0 + j) : 0.f;
-        if (ACC) old[j] = j < n ? to_f32(y[j * p.ldy]) : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        float v = int8_value(acc[j], s[j], sw);
-        if (!ok) v = __int_as_float(0x7fc00000);
-        if (ACC) v += old[j];
-        if (j < n) y[j * p.ldy] = from_f32<Y>(v);
-    }
+__device__ __forceinline__ int4 add4(const int4& a, const int4& b) {
+    return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 template <typename Y, bool ACC>
-__global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_constant__ CUtensorMap map_w,
-                                                              const __grid_constant__ CUtensorMap map_x,
-                                                              const __grid_constant__ Int8TcArgs a) {
+__global__ void __launch_bounds__(kI8Threads)
+    fluxbin_int8_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                           const __grid_constant__ CUtensorMap map_y, const __grid_constant__ Int8TcArgs a) {
     const Int8Args& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sb = smem_base();
@@ -194,6 +181,7 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
     const int tile_t = (int)(tile % (unsigned)a.tiles_t), tile_m = (int)(tile / (unsigned)a.tiles_t);
     const int kb0 = (int)((int64_t)a.kblocks * rank / a.splits), kb1 = (int)((int64_t)a.kblocks * (rank + 1) / a.splits);
     const int nk = kb1 - kb0;
+    const int m0 = tile_m * kI8Rows;
 
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kSlot),
@@ -216,33 +204,46 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
     const uint32_t tmem = smem_at<const uint32_t>(kSlot);
     const bool aligned = (sb & 1023u) == 0;
 
-    if (warp == 0 && lane == 0 && aligned) {
+    if (warp == 0 && aligned) {
         // ---- copies ----
         bool ok = true;
         const bool early = (p.flags & kInt8Early) != 0;
         const int ahead = nk < a.stages ? nk : a.stages;
         const int nload = a.test_stall ? 0 : nk;
-        int i = 0;
         if (early && nload) {
             // the ring's first weights before the preceding kernel has finished
             for (int s = 0; s < ahead; ++s) {
-                int8_expect(full0 + 8 * s, stage_bytes);
-                int8_tma(ring + s * stage_bytes, &map_w, (kb0 + s) * kI8K, tile_m * kI8Rows, full0 + 8 * s);
+                if (elect_one()) {
+                    int8_expect(full0 + 8 * s, stage_bytes);
+                    int8_tma(ring + s * stage_bytes, &map_w, (kb0 + s) * kI8K, m0, full0 + 8 * s);
+                }
+                __syncwarp();
             }
         }
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        for (; i < nload && ok; ++i) {
-            const int s = i % a.stages;
-            const uint32_t dst = ring + s * stage_bytes;
-            if (i >= a.stages) ok = tc_mbar_wait(empty0 + 8 * s, (uint32_t)(i / a.stages - 1) & 1u, a.spin_limit);
-            if (!ok) break;
-            if (!early || i >= ahead) {
-                int8_expect(full0 + 8 * s, stage_bytes);
-                int8_tma(dst, &map_w, (kb0 + i) * kI8K, tile_m * kI8Rows, full0 + 8 * s);
+        int i = 0, s = 0;
+        uint32_t round = 0;                      // times the ring has been filled before
+        for (; i < nload; ++i) {
+            if (round > 0) {
+                ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
             }
-            int8_tma(dst + kI8Rows * kI8K, &map_x, (kb0 + i) * kI8K, tile_t * a.bn, full0 + 8 * s);
+            if (elect_one()) {
+                const uint32_t dst = ring + s * stage_bytes;
+                if (!early || i >= ahead) {
+                    int8_expect(full0 + 8 * s, stage_bytes);
+                    int8_tma(dst, &map_w, (kb0 + i) * kI8K, m0, full0 + 8 * s);
+                }
+                int8_tma(dst + kI8Rows * kI8K, &map_x, (kb0 + i) * kI8K, tile_t * a.bn, full0 + 8 * s);
+            }
+            __syncwarp();
+            if (++s == a.stages) {
+                s = 0;
+                ++round;
+            }
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
             atomicOr(a.err, 1u);
             smem_at<uint32_t>(kFailed) = 1u;
         }
@@ -253,9 +254,10 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
         // ---- matrix instructions ----
         const uint32_t idesc = int8_idesc(kI8Rows, a.bn);
         bool ok = true;
+        int s = 0;
+        uint32_t round = 0;
         for (int i = 0; i < nk; ++i) {
-            const int s = i % a.stages;
-            ok = tc_mbar_wait(full0 + 8 * s, (uint32_t)(i / a.stages) & 1u, a.spin_limit);
+            ok = tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (elect_one()) {
@@ -266,6 +268,10 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
                 tc_commit(empty0 + 8 * s);
             }
             __syncwarp();
+            if (++s == a.stages) {
+                s = 0;
+                ++round;
+            }
         }
         if (elect_one()) {
             tc_commit(done);   // every instruction issued above has finished (at once when there is none)
@@ -276,6 +282,22 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
         }
     }
     __syncwarp();
+    // scales are read and outputs written after the preceding kernel; they
+    // are on their way while the products run
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t t0 = (int64_t)tile_t * a.bn;
+    const int nt = (int)(p.T - t0 < a.bn ? p.T - t0 : a.bn);
+    if (tid < a.bn) smem_at<float>(kI8SxOff + 4 * tid) = tid < nt ? __ldg(p.sx + t0 + tid) : 0.f;
+    const int quarter = warp & 3;                // the lanes of tensor memory that this warp reaches
+    const int row = quarter * 32 + lane, m = m0 + row;
+    const int mq = 4 * lane;                     // the four channels of the split's sums
+    float sw4[4];
+    if (a.splits == 1) {
+        sw4[0] = m < p.M ? __ldg(p.sw + m) : 0.f;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sw4[j] = m0 + mq + j < p.M ? __ldg(p.sw + m0 + mq + j) : 0.f;
+    }
     // every thread waits for the accumulators; the full limit even under the
     // test hook, since nothing may release them under running instructions
     const bool drained = aligned ? tc_mbar_wait(done, 0u, kI8SpinLimit) : true;
@@ -283,72 +305,101 @@ __global__ void __launch_bounds__(128) fluxbin_int8_tc_kernel(const __grid_const
         atomicOr(a.err, drained ? 1u : 2u);
         smem_at<uint32_t>(kFailed) = 1u;
     }
-    // outputs are written (and scales read) after the preceding kernel
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
     tc_fence_after();
     const bool ok = drained && smem_at<const volatile uint32_t>(kFailed) == 0u;
 
-    const int row = warp * 32 + lane;            // this thread's lane of the accumulators
-    const int m = tile_m * kI8Rows + row;
-    const int64_t t0 = (int64_t)tile_t * a.bn;
-    const uint32_t acc0 = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t red = ring;                   // [bn][128] partial sums (every stage has been consumed)
-    if (a.splits == 1) {
-        const float sw = m < p.M ? p.sw[m] : 0.f;
-        for (int c = 0; c < a.bn; c += 16) {
-            int v[16];
-            int8_ld16(acc0 + (uint32_t)c, v);
-            tc_wait_ld();
-            if (m < p.M && t0 + c < p.T) int8_store16<Y, ACC>(p, t0 + c, m, sw, v, ok);
-        }
-    } else {
-        for (int c = 0; c < a.bn; c += 16) {
-            int v[16];
-            int8_ld16(acc0 + (uint32_t)c, v);
-            tc_wait_ld();
+    const uint32_t acc0 = tmem + ((uint32_t)(quarter * 32) << 16);
+    const bool bulk = !ACC && a.splits == 1 && a.bulk > (m0 + kI8Rows <= p.M ? 0 : 1);
+    // Every stage has been consumed: the ring holds the partial sums
+    // ([bn][128] integers), or the tile of y on its way out ([bn][128] of Y).
+    // Groups of 16 tokens, alternately to the two warps that reach a quarter.
+    for (int g = warp >> 2; g < a.bn / 16; g += 2) {
+        const int c = 16 * g;
+        int v[16];
+        int8_ld16(acc0 + (uint32_t)c, v);
+        tc_wait_ld();
+        if (a.splits > 1) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) smem_at<int>(kI8RingOff + ((c + j) * kI8Rows + row) * 4) = v[j];
+            for (int j = 0; j < 16; ++j) smem_at<int>((uint32_t)(kI8RingOff + ((c + j) * kI8Rows + row) * 4)) = v[j];
+            continue;
+        }
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const float4 s4 = smem_at<const float4>((uint32_t)(kI8SxOff + 4 * (c + j)));
+            f[j] = int8_value(v[j], s4.x, sw4[0]);
+            f[j + 1] = int8_value(v[j + 1], s4.y, sw4[0]);
+            f[j + 2] = int8_value(v[j + 2], s4.z, sw4[0]);
+            f[j + 3] = int8_value(v[j + 3], s4.w, sw4[0]);
+        }
+        if (!ok) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = __int_as_float(0x7fc00000);
+        }
+        if (bulk) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                smem_at<Y>((uint32_t)(kI8RingOff + ((c + j) * kI8Rows + row) * (int)sizeof(Y))) = from_f32<Y>(f[j]);
+        } else if (m < p.M) {
+            Y* y = static_cast<Y*>(p.y) + (t0 + c) * p.ldy + m;
+            float old[16];
+            if (ACC) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) old[j] = c + j < nt ? to_f32(y[j * p.ldy]) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < nt) y[j * p.ldy] = from_f32<Y>(ACC ? f[j] + old[j] : f[j]);
         }
     }
+    if (bulk) fence_async_smem();
     tc_fence_before();
     __syncthreads();
     if (warp == 1 && drained) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols));
     }
+    if (bulk) {
+        if (tid == 0) {
+            for (int c = 0; c < nt; c += kI8OutBox)
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                             ::"l"(&map_y), "r"(m0), "r"((int)(t0 + c)), "r"(ring + (uint32_t)(c * kI8Rows * (int)sizeof(Y)))
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+        }
+    }
     if (a.splits > 1) {
         int8_cluster_sync();
-        // this CTA's share of the tile's (token, four channels) items, added
-        // over the cluster
+        // this CTA's share of the tile's tokens, added over the cluster: a
+        // warp has the 128 channels of a token, four a lane
         bool all_ok = true;
         for (int r = 0; r < a.splits; ++r) all_ok = all_ok && ld_dsmem(dsmem_addr(sb + kFailed, r)) == 0;
-        const int nt = (int)(p.T - t0 < a.bn ? p.T - t0 : a.bn);
-        const int items = nt * (kI8Rows / 4);
-        const int i0 = items * rank / a.splits, i1 = items * (rank + 1) / a.splits;
-        uint32_t peer[8];
+        uint32_t peer[kI8MaxSplits];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) peer[r] = dsmem_addr(red, r < a.splits ? r : 0);
-        for (int i = i0 + tid; i < i1; i += 128) {
-            const int c = i / (kI8Rows / 4), mq = 4 * (i % (kI8Rows / 4)), mg = tile_m * kI8Rows + mq;
-            int4 part[8];
+        for (int r = 0; r < kI8MaxSplits; ++r) peer[r] = dsmem_addr(ring + (uint32_t)(mq * 4), r < a.splits ? r : 0);
+        const int c0 = nt * rank / a.splits, c1 = nt * (rank + 1) / a.splits;
+        for (int c = c0 + warp; c < c1; c += 2 * (kI8Threads / 32)) {
+            // two tokens at a time: their loads overlap
+            const int cb = c + kI8Threads / 32;
+            int4 part[2][kI8MaxSplits];
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < a.splits) part[r] = ld_dsmem4(peer[r] + (uint32_t)((c * kI8Rows + mq) * 4));
-            float sw4[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sw4[j] = mg + j < p.M ? __ldg(p.sw + mg + j) : 0.f;
-            const float sxv = __ldg(p.sx + t0 + c);
-            int4 v = part[0];
-#pragma unroll
-            for (int r = 1; r < 8; ++r)
+            for (int r = 0; r < kI8MaxSplits; ++r)
                 if (r < a.splits) {
-                    v.x += part[r].x;
-                    v.y += part[r].y;
-                    v.z += part[r].z;
-                    v.w += part[r].w;
+                    part[0][r] = ld_dsmem4(peer[r] + (uint32_t)(c * kI8Rows * 4));
+                    if (cb < c1) part[1][r] = ld_dsmem4(peer[r] + (uint32_t)(cb * kI8Rows * 4));
                 }
-            if (mg < p.M) int8_store4<Y, ACC>(p, t0 + c, mg, sxv, sw4, v, all_ok);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int ch = h ? cb : c;
+                if (ch >= c1 || m0 + mq >= p.M) continue;
+                int4 v = part[h][0];
+#pragma unroll
+                for (int r = 1; r < kI8MaxSplits; ++r)
+                    if (r < a.splits) v = add4(v, part[h][r]);
+                int8_store4<Y, ACC>(p, t0 + ch, m0 + mq, smem_at<const float>((uint32_t)(kI8SxOff + 4 * ch)), sw4, v,
+                                    all_ok);
+            }
         }
         int8_cluster_sync();                     // the others have read this CTA's sums
     }

@@ -45,7 +45,8 @@ struct Int8PairArgs {
 __host__ __device__ constexpr int int8_pair_stage_bytes(int bn) { return kI8Rows * kI8K + (bn / 2) * kI8K; }
 // Always sized for the widest tile and y: all of an SM's shared memory.
 constexpr int kI8PairChunk = 32;         // tokens staged at a time
-constexpr int kI8PairOutOff = kI8RingOff + kI8PairStages * int8_pair_stage_bytes(kI8MaxBn);
+constexpr int kI8PairRingOff = 1024;
+constexpr int kI8PairOutOff = kI8PairRingOff + kI8PairStages * int8_pair_stage_bytes(kI8MaxBn);
 constexpr int kI8PairOutBytes = kI8PairChunk * kI8Rows * 4;        // one of two staging buffers
 constexpr int kI8PairSxOff = kI8PairOutOff + 2 * kI8PairOutBytes;  // [2][256] token scales
 constexpr int kI8PairSmem = kI8PairSxOff + 2 * kI8MaxBn * 4;
@@ -120,7 +121,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
     const uint32_t full0 = sb, empty0 = sb + 64, acc_full0 = sb + 128, acc_empty0 = sb + 144, done = sb + 160,
                    y_full0 = sb + 168;
     constexpr uint32_t kSlot = 184, kDrained = 188;
-    const uint32_t ring = sb + kI8RingOff;
+    const uint32_t ring = sb + kI8PairRingOff;
     const uint32_t stage_bytes = (uint32_t)int8_pair_stage_bytes(a.bn);
     const int rank = (int)(blockIdx.x & 1);
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -153,18 +154,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
     bool ok = aligned;
 
     if (warp == 0) {
-        if (lane == 0 && aligned) {
+        if (aligned) {
             // ---- copies: this CTA's half of the channels and of the tokens ----
             const bool early = (p.flags & kInt8Early) != 0;
             const int half = a.bn / 2;
+            const uint32_t bar0 = dsmem_addr(full0, 0);   // the leader's full barriers
             int pre = 0;                           // stages whose weights were requested early
             if (early && !a.test_stall && first < a.tiles) {
                 const Int8PairTile t = int8_pair_tile(a, first);
                 pre = a.kblocks < kI8PairStages ? a.kblocks : kI8PairStages;
                 for (int s = 0; s < pre; ++s) {
-                    if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
-                    int8_pair_tma(ring + s * stage_bytes, &map_w, s * kI8K, t.tm * 2 * kI8Rows + rank * kI8Rows,
-                                  dsmem_addr(full0 + 8 * s, 0));
+                    if (elect_one()) {
+                        if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
+                        int8_pair_tma(ring + s * stage_bytes, &map_w, s * kI8K, (t.tm * 2 + rank) * kI8Rows, bar0 + 8 * s);
+                    }
+                    __syncwarp();
                 }
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -172,16 +176,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             uint32_t round = 0;                    // times the ring has been filled before
             for (int64_t i = first; i < a.tiles && ok && !a.test_stall; i += step) {
                 const Int8PairTile t = int8_pair_tile(a, i);
+                const int wy = (t.tm * 2 + rank) * kI8Rows, xy = t.tt * a.bn + rank * half;
                 for (int k = 0; k < a.kblocks; ++k) {
-                    const uint32_t bar = dsmem_addr(full0 + 8 * s, 0), dst = ring + s * stage_bytes;
-                    if (round > 0 && !(ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit))) break;
-                    if (pre > 0) {
-                        --pre;
-                    } else {
-                        if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
-                        int8_pair_tma(dst, &map_w, k * kI8K, t.tm * 2 * kI8Rows + rank * kI8Rows, bar);
+                    if (round > 0) {
+                        ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
                     }
-                    int8_pair_tma(dst + kI8Rows * kI8K, &map_x, k * kI8K, t.tt * a.bn + rank * half, bar);
+                    if (elect_one()) {
+                        const uint32_t dst = ring + s * stage_bytes;
+                        if (pre == 0) {
+                            if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
+                            int8_pair_tma(dst, &map_w, k * kI8K, wy, bar0 + 8 * s);
+                        }
+                        int8_pair_tma(dst + kI8Rows * kI8K, &map_x, k * kI8K, xy, bar0 + 8 * s);
+                    }
+                    __syncwarp();
+                    if (pre > 0) --pre;
                     if (++s == kI8PairStages) {
                         s = 0;
                         ++round;
@@ -189,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 }
             }
             if (!ok) {
-                atomicOr(a.err, 1u);
+                if (lane == 0) atomicOr(a.err, 1u);
                 // the copies in flight land within microseconds; the leader's
                 // barriers cannot be waited for from the other CTA, so a copier
                 // that gave up stays for a millisecond
