@@ -206,74 +206,61 @@ __global__ void __launch_bounds__(kI8Threads)
 
     if (warp == 0 && aligned) {
         // ---- copies ----
-        bool ok = true;
-        const bool early = (p.flags & kInt8Early) != 0;
-        const int ahead = nk < a.stages ? nk : a.stages;
-        const int nload = a.test_stall ? 0 : nk;
-        if (early && nload) {
-            // the ring's first weights before the preceding kernel has finished
-            for (int s = 0; s < ahead; ++s) {
-                if (elect_one()) {
+        if (elect_one()) {
+            bool ok = true;
+            const bool early = (p.flags & kInt8Early) != 0;
+            const int ahead = nk < a.stages ? nk : a.stages;
+            const int nload = a.test_stall ? 0 : nk;
+            if (early && nload) {
+                // the ring's first weights before the preceding kernel has finished
+                for (int s = 0; s < ahead; ++s) {
                     int8_expect(full0 + 8 * s, stage_bytes);
                     int8_tma(ring + s * stage_bytes, &map_w, (kb0 + s) * kI8K, m0, full0 + 8 * s);
                 }
-                __syncwarp();
             }
-        }
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        int i = 0, s = 0;
-        uint32_t round = 0;                      // times the ring has been filled before
-        for (; i < nload; ++i) {
-            if (round > 0) {
-                ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-            }
-            if (elect_one()) {
-                const uint32_t dst = ring + s * stage_bytes;
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int i = 0, s = 0;
+            uint32_t round = 0;                  // times the ring has been filled before
+            for (; i < nload; ++i) {
+                if (round > 0 && !(ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit))) break;
+                const uint32_t dst = ring + s * stage_bytes, bar = full0 + 8 * s;
                 if (!early || i >= ahead) {
-                    int8_expect(full0 + 8 * s, stage_bytes);
-                    int8_tma(dst, &map_w, (kb0 + i) * kI8K, m0, full0 + 8 * s);
+                    int8_expect(bar, stage_bytes);
+                    int8_tma(dst, &map_w, (kb0 + i) * kI8K, m0, bar);
                 }
-                int8_tma(dst + kI8Rows * kI8K, &map_x, (kb0 + i) * kI8K, tile_t * a.bn, full0 + 8 * s);
+                int8_tma(dst + kI8Rows * kI8K, &map_x, (kb0 + i) * kI8K, tile_t * a.bn, bar);
+                if (++s == a.stages) {
+                    s = 0;
+                    ++round;
+                }
             }
-            __syncwarp();
-            if (++s == a.stages) {
-                s = 0;
-                ++round;
+            if (!ok) {
+                atomicOr(a.err, 1u);
+                smem_at<uint32_t>(kFailed) = 1u;
             }
+            // copies in flight land before the CTA ends: the last fill of every stage
+            for (int k = i > a.stages ? i - a.stages : 0; k < i; ++k)
+                (void)tc_mbar_wait(full0 + 8 * (k % a.stages), (uint32_t)(k / a.stages) & 1u, kI8SpinLimit);
         }
-        if (!ok && lane == 0) {
-            atomicOr(a.err, 1u);
-            smem_at<uint32_t>(kFailed) = 1u;
-        }
-        // copies in flight land before the CTA ends: the last fill of every stage
-        for (int k = i > a.stages ? i - a.stages : 0; k < i; ++k)
-            (void)tc_mbar_wait(full0 + 8 * (k % a.stages), (uint32_t)(k / a.stages) & 1u, kI8SpinLimit);
     } else if (warp == 1 && aligned) {
         // ---- matrix instructions ----
-        const uint32_t idesc = int8_idesc(kI8Rows, a.bn);
-        bool ok = true;
-        int s = 0;
-        uint32_t round = 0;
-        for (int i = 0; i < nk; ++i) {
-            ok = tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (elect_one()) {
+        if (elect_one()) {
+            const uint32_t idesc = int8_idesc(kI8Rows, a.bn);
+            bool ok = true;
+            int s = 0;
+            uint32_t round = 0;
+            for (int i = 0; i < nk; ++i) {
+                if (!(ok = tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit))) break;
                 const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
                 const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) int8_mma(tmem, da + 2 * k, db + 2 * k, idesc, i > 0 || k > 0);
                 tc_commit(empty0 + 8 * s);
+                if (++s == a.stages) {
+                    s = 0;
+                    ++round;
+                }
             }
-            __syncwarp();
-            if (++s == a.stages) {
-                s = 0;
-                ++round;
-            }
-        }
-        if (elect_one()) {
             tc_commit(done);   // every instruction issued above has finished (at once when there is none)
             if (!ok) {
                 atomicOr(a.err, 1u);

@@ -154,7 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
     bool ok = aligned;
 
     if (warp == 0) {
-        if (aligned) {
+        if (aligned && elect_one()) {
             // ---- copies: this CTA's half of the channels and of the tokens ----
             const bool early = (p.flags & kInt8Early) != 0;
             const int half = a.bn / 2;
@@ -164,11 +164,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 const Int8PairTile t = int8_pair_tile(a, first);
                 pre = a.kblocks < kI8PairStages ? a.kblocks : kI8PairStages;
                 for (int s = 0; s < pre; ++s) {
-                    if (elect_one()) {
-                        if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
-                        int8_pair_tma(ring + s * stage_bytes, &map_w, s * kI8K, (t.tm * 2 + rank) * kI8Rows, bar0 + 8 * s);
-                    }
-                    __syncwarp();
+                    if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
+                    int8_pair_tma(ring + s * stage_bytes, &map_w, s * kI8K, (t.tm * 2 + rank) * kI8Rows, bar0 + 8 * s);
                 }
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -178,21 +175,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 const Int8PairTile t = int8_pair_tile(a, i);
                 const int wy = (t.tm * 2 + rank) * kI8Rows, xy = t.tt * a.bn + rank * half;
                 for (int k = 0; k < a.kblocks; ++k) {
-                    if (round > 0) {
-                        ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
+                    if (round > 0 && !(ok = tc_mbar_wait(empty0 + 8 * s, (round - 1) & 1u, a.spin_limit))) break;
+                    const uint32_t dst = ring + s * stage_bytes, bar = bar0 + 8 * s;
+                    if (pre > 0) {
+                        --pre;
+                    } else {
+                        if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
+                        int8_pair_tma(dst, &map_w, k * kI8K, wy, bar);
                     }
-                    if (elect_one()) {
-                        const uint32_t dst = ring + s * stage_bytes;
-                        if (pre == 0) {
-                            if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
-                            int8_pair_tma(dst, &map_w, k * kI8K, wy, bar0 + 8 * s);
-                        }
-                        int8_pair_tma(dst + kI8Rows * kI8K, &map_x, k * kI8K, xy, bar0 + 8 * s);
-                    }
-                    __syncwarp();
-                    if (pre > 0) --pre;
+                    int8_pair_tma(dst + kI8Rows * kI8K, &map_x, k * kI8K, xy, bar);
                     if (++s == kI8PairStages) {
                         s = 0;
                         ++round;
@@ -200,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 }
             }
             if (!ok) {
-                if (lane == 0) atomicOr(a.err, 1u);
+                atomicOr(a.err, 1u);
                 // the copies in flight land within microseconds; the leader's
                 // barriers cannot be waited for from the other CTA, so a copier
                 // that gave up stays for a millisecond
@@ -208,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && aligned) {
+        if (rank == 0 && aligned && elect_one()) {
             // ---- matrix instructions, for both CTAs ----
             const uint32_t idesc = int8_idesc(2 * kI8Rows, a.bn);
             int s = 0;
@@ -216,33 +207,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             int64_t n = 0;                         // tiles so far
             for (int64_t i = first; i < a.tiles && ok; i += step, ++n) {
                 const int b = (int)(n & 1);
-                if (n >= 2) ok = tc_mbar_wait(acc_empty0 + 8 * b, (uint32_t)((n >> 1) - 1) & 1u, a.spin_limit);
+                if (n >= 2 && !(ok = tc_mbar_wait(acc_empty0 + 8 * b, (uint32_t)((n >> 1) - 1) & 1u, a.spin_limit))) break;
                 tc_fence_after();
                 for (int k = 0; k < a.kblocks; ++k) {
-                    ok = ok && tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
-                        const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
+                    if (!(ok = tc_mbar_wait(full0 + 8 * s, round & 1u, a.spin_limit))) break;
+                    const uint64_t da = tc_smem_desc_sw128(ring + s * stage_bytes);
+                    const uint64_t db = tc_smem_desc_sw128(ring + s * stage_bytes + kI8Rows * kI8K);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            int8_pair_mma(tmem + (uint32_t)(b * kI8MaxBn), da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
-                        int8_pair_commit(empty0 + 8 * s);
-                    }
-                    __syncwarp();
+                    for (int q = 0; q < 4; ++q)
+                        int8_pair_mma(tmem + (uint32_t)(b * kI8MaxBn), da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
+                    int8_pair_commit(empty0 + 8 * s);
                     if (++s == kI8PairStages) {
                         s = 0;
                         ++round;
                     }
                 }
-                if (ok && elect_one()) int8_pair_commit(acc_full0 + 8 * b);
-                __syncwarp();
+                if (ok) int8_pair_commit(acc_full0 + 8 * b);
             }
-            if (elect_one()) {
-                int8_pair_commit(done);            // every instruction issued above has finished
-                if (!ok) atomicOr(a.err, 1u);
-            }
+            int8_pair_commit(done);                // every instruction issued above has finished
+            if (!ok) atomicOr(a.err, 1u);
         }
     } else {
         // ---- outputs ----
