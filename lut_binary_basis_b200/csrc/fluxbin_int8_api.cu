@@ -65,23 +65,16 @@ int launch(K kernel, dim3 grid, dim3 block, size_t smem, int cluster, void* stre
 
 using QuantFn = void (*)(QuantArgs);
 
-template <int KIND, typename E, typename H>
-QuantFn pick_quant(int vpt, bool vec) {
-    if (vec) {
-        switch (vpt) {
-            case 1: return &fluxbin_quant_kernel<KIND, E, H, 1, true>;
-            case 2: return &fluxbin_quant_kernel<KIND, E, H, 2, true>;
-            case 4: return &fluxbin_quant_kernel<KIND, E, H, 4, true>;
-            default: return &fluxbin_quant_kernel<KIND, E, H, 0, true>;
-        }
-    }
+template <int KIND, typename E, typename H, bool VEC>
+QuantFn pick_quant(int vpt) {
     switch (vpt) {
-        case 1: return &fluxbin_quant_kernel<KIND, E, H, 1, false>;
-        case 2: return &fluxbin_quant_kernel<KIND, E, H, 2, false>;
-        case 4: return &fluxbin_quant_kernel<KIND, E, H, 4, false>;
-        default: return &fluxbin_quant_kernel<KIND, E, H, 0, false>;
+        case 1: return &fluxbin_quant_kernel<KIND, E, H, 1, VEC>;
+        case 2: return &fluxbin_quant_kernel<KIND, E, H, 2, VEC>;
+        default: return &fluxbin_quant_kernel<KIND, E, H, 4, VEC>;
     }
 }
+template <int KIND, typename E, typename H>
+QuantFn pick_quant(int vpt, bool vec) { return vec ? pick_quant<KIND, E, H, true>(vpt) : pick_quant<KIND, E, H, false>(vpt); }
 
 // Checks what the three operators share and launches.  `in0`, `in1` (delta or
 // up, may be null), `gamma` and `h_out` as the operator has them.
@@ -124,12 +117,14 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     a.eps = eps;
     const bool vec = N % 8 == 0 && in0.rows_aligned16() && (!in1.p || in1.rows_aligned16()) &&
                      (!gamma || ptr_aligned(gamma, 16)) && (!h_out.p || h_out.rows_aligned16());
-    // threads of a row: enough for one vector of 8 elements each, up to 1024
     const int64_t vecs = (N + 7) / 8;
-    int tpr = 32;
-    while (tpr < 1024 && tpr < vecs) tpr *= 2;
-    const int64_t per = (vecs + tpr - 1) / tpr;
-    const int vpt = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 0;
+    int vpt = 1;
+    while (vpt < 4 && vecs > (int64_t)vpt * quant_max_threads(vpt)) vpt *= 2;
+    int parts = 1;
+    while (vecs > (int64_t)parts * vpt * quant_max_threads(vpt)) parts *= 2;
+    const int64_t per_thread = (int64_t)parts * vpt;
+    const int tpr = std::max(32, (int)(((vecs + per_thread - 1) / per_thread + 31) / 32 * 32));
+    a.parts = parts;
     const int rpc = tpr >= 128 ? 1 : 128 / tpr;
     const bool bf = (flags & FLUXBIN_FLAG_BF16) != 0;
     QuantFn fn;
@@ -142,7 +137,9 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     } else {
         fn = bf ? pick_quant<KIND, __nv_bfloat16, __nv_bfloat16>(vpt, vec) : pick_quant<KIND, __half, __half>(vpt, vec);
     }
-    return launch(fn, dim3((unsigned)((T + rpc - 1) / rpc)), dim3((unsigned)tpr, (unsigned)rpc), 0, 1, stream, a);
+    const int64_t blocks = (T + rpc - 1) / rpc * parts;
+    if (blocks > INT32_MAX) return FLUXBIN_ERR_UNSUPPORTED;
+    return launch(fn, dim3((unsigned)blocks), dim3((unsigned)tpr, (unsigned)rpc), 0, parts, stream, a);
 }
 
 // ---------------------------------------------------------------------------

@@ -21,12 +21,16 @@
 // taken over the bit patterns of |v| as integers, whose order is that of the
 // values with NaN above infinity, so a NaN is never lost in it.
 //
-// Bound: memory (one read of each input, one write of each output).  A row is
-// owned by blockDim.x threads and stays in their registers between the
-// reductions and the codes (VPT vectors of 8 elements a thread); rows of more
-// than 32,768 elements are read twice (VPT = 0).  Rows that allow 16-byte
-// accesses take them (VEC); others are read element by element with
-// consecutive threads on consecutive elements.
+// Bound: memory (one read of each input, one write of each output).  A row
+// stays in its threads' registers between the reductions and the codes: VPT
+// vectors of 8 consecutive elements a thread, blockDim.x threads a CTA and,
+// for rows that one CTA does not hold, the CTAs of a cluster, which exchange
+// their maxima and sums through distributed shared memory.  Rows that start
+// off a 16-byte boundary are read with aligned 16-byte loads that are shifted
+// into place, and written with 16-byte stores put together from two
+// neighbouring threads' elements (an SM gets a store away every 13 to 20
+// clocks, however narrow it is); only the ends of such a row go element by
+// element.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -49,172 +53,343 @@ struct QuantArgs {
     int64_t lda, ldb, ldo, ldq;
     int32_t T, N;
     float eps;
+    int32_t parts;        // CTAs (of one cluster) that share a row
 };
 
-// 8 consecutive elements at a 16-byte boundary.
+// --- pairs of fp32 (one instruction for both) -------------------------------
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// max(m, |a|, |b|), NaN if any is.
+__device__ __forceinline__ float max_abs(float m, uint64_t ab) {
+    const float2 f = unpair(ab);
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(f.x)), "f"(fabsf(f.y)));
+    return r;
+}
+
+// --- eight elements of a row ------------------------------------------------
+
+// Their bits, two 16-bit values or one fp32 a word.
 template <typename T>
-struct alignas(16) Vec8 {
-    T v[8];
+struct Raw {
+    static constexpr int kWords = 8 * sizeof(T) / 4;
+    uint32_t w[kWords];
 };
 
-// Element j of a thread's chunk i: 8 consecutive elements (VEC), or elements
-// one row of threads apart.
-template <bool VEC>
-__device__ __forceinline__ int quant_index(int i, int j, int tpr) {
-    return VEC ? (i * tpr + (int)threadIdx.x) * 8 + j : (i * 8 + j) * tpr + (int)threadIdx.x;
+// The 16 bytes that start `by` bytes (below 16, a multiple of 2) into w[K..K+7].
+template <int K>
+__device__ __forceinline__ uint4 shifted(const uint32_t* w, uint32_t by) {
+    uint32_t x[6], y[5], r[4];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) x[k] = (by & 8u) ? w[K + k + 2] : w[K + k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) y[k] = (by & 4u) ? x[k + 1] : x[k];
+    const uint32_t sel = (by & 2u) ? 0x5432u : 0x3210u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = __byte_perm(y[k], y[k + 1], sel);
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+__device__ __forceinline__ void put(uint32_t* w, const uint4& v) {
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+}
+
+// Elements n .. n+7 of a row of N (zeros past its end).  VEC: the row's
+// length is a multiple of 8 and it starts at a 16-byte boundary.
 template <bool VEC, typename T>
-__device__ __forceinline__ void quant_load(const T* row, int i, int tpr, int N, float (&f)[8]) {
+__device__ __forceinline__ Raw<T> quant_load(const T* row, int n, int N) {
+    constexpr int U = Raw<T>::kWords / 4;                       // 16-byte units of the eight elements
+    Raw<T> x;
     if constexpr (VEC) {
-        const int n = quant_index<true>(i, 0, tpr);
-        Vec8<T> x;
-        if (n < N) {
-            x = *reinterpret_cast<const Vec8<T>*>(row + n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (n < N) v = reinterpret_cast<const uint4*>(row + n)[u];
+            put(x.w + 4 * u, v);
+        }
+    } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + n);
+        const uint32_t off = (uint32_t)at & 15u;                // the same for the whole row
+        const int before = (int)(off / sizeof(T)), after = off ? (int)((16u - off) / sizeof(T)) : 0;
+        if (n >= before && n + 8 + after <= N) {
+            // whole aligned units, all of them within the row
+            const uint4* from = reinterpret_cast<const uint4*>(at - off);
+            uint32_t w[4 * U + 4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) put(w + 4 * u, from[u]);
+            put(w + 4 * U, off ? from[U] : make_uint4(0, 0, 0, 0));
+            put(x.w, shifted<0>(w, off));
+            if constexpr (U == 2) put(x.w + 4, shifted<4>(w, off));
         } else {
+            uint32_t e[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x.v[j] = from_f32<T>(0.f);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = to_f32(x.v[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int n = quant_index<false>(i, j, tpr);
-            f[j] = n < N ? to_f32(row[n]) : 0.f;
-        }
-    }
-}
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void quant_store(T* row, int i, int tpr, int N, const float (&f)[8]) {
-    if constexpr (VEC) {
-        const int n = quant_index<true>(i, 0, tpr);
-        Vec8<T> x;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x.v[j] = from_f32<T>(f[j]);
-        if (n < N) *reinterpret_cast<Vec8<T>*>(row + n) = x;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int n = quant_index<false>(i, j, tpr);
-            if (n < N) row[n] = from_f32<T>(f[j]);
-        }
-    }
-}
-
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    // exp(-g) overflows to infinity below g = -88 and its reciprocal is then
-    // 0: silu's own limit.  The approximate exponential and reciprocal are
-    // within a few 2^-23 of the value, far below half a step of 8 bits.
-    float rc;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(rc) : "f"(1.f + __expf(-g)));
-    return g * rc * u;
-}
-
-// The row's values before the common factor (chunk i).  rmsnorm: adds the
-// residual, writes h' (FIRST) and sums its squares; a second pass reads h'
-// back when it was written (h_out may be h itself).
-template <int KIND, typename E, typename H, bool VEC, bool FIRST>
-__device__ __forceinline__ void quant_values(const QuantArgs& p, int64_t t, int i, int tpr, float (&f)[8], float& ss) {
-    if constexpr (KIND == kQuantQuant) {
-        quant_load<VEC>(static_cast<const E*>(p.a) + t * p.lda, i, tpr, p.N, f);
-    } else if constexpr (KIND == kQuantSilu) {
-        float u[8];
-        quant_load<VEC>(static_cast<const E*>(p.a) + t * p.lda, i, tpr, p.N, f);
-        quant_load<VEC>(static_cast<const E*>(p.b) + t * p.ldb, i, tpr, p.N, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = silu_mul(f[j], u[j]);
-    } else {
-        float g[8];
-        if (FIRST || !p.h_out) {
-            quant_load<VEC>(static_cast<const H*>(p.a) + t * p.lda, i, tpr, p.N, f);
-            if (p.b) {
-                float d[8];
-                quant_load<VEC>(static_cast<const E*>(p.b) + t * p.ldb, i, tpr, p.N, d);
-                // rounded once to the stream's own type: the norm and every
-                // later reader of the stream see the same h'
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = to_f32(from_f32<H>(f[j] + d[j]));
+            for (int j = 0; j < 8; ++j) {
+                e[j] = 0u;
+                if (n + j < N) {
+                    if constexpr (U == 1) e[j] = *reinterpret_cast<const unsigned short*>(row + n + j);
+                    else e[j] = *reinterpret_cast<const uint32_t*>(row + n + j);
+                }
             }
-            if (FIRST && p.h_out) quant_store<VEC>(static_cast<H*>(p.h_out) + t * p.ldo, i, tpr, p.N, f);
-        } else {
-            quant_load<VEC>(static_cast<const H*>(p.h_out) + t * p.ldo, i, tpr, p.N, f);
+#pragma unroll
+            for (int k = 0; k < 4 * U; ++k)
+                x.w[k] = U == 1 ? __byte_perm(e[(2 * k) % 8], e[(2 * k + 1) % 8], 0x5410) : e[k % 8];
         }
-        quant_load<VEC>(static_cast<const E*>(p.gamma), i, tpr, p.N, g);
+    }
+    return x;
+}
+
+template <typename T>
+__device__ __forceinline__ void put_element(T* at, const Raw<T>& x, int j) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<unsigned short*>(at) = (unsigned short)(x.w[j / 2] >> (16 * (j % 2)));
+    else *reinterpret_cast<uint32_t*>(at) = x.w[j % Raw<T>::kWords];
+}
+
+// Writes them.  All 32 lanes take part: lane l has the eight elements after
+// lane l-1's.
+template <bool VEC, typename T>
+__device__ __forceinline__ void quant_store(T* row, int n, int N, const Raw<T>& x) {
+    constexpr int U = Raw<T>::kWords / 4;
+    if constexpr (VEC) {
+        if (n < N) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                reinterpret_cast<uint4*>(row + n)[u] =
+                    make_uint4(x.w[4 * u], x.w[4 * u + 1], x.w[4 * u + 2], x.w[4 * u + 3]);
+        }
+    } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + n);
+        const uint32_t off = (uint32_t)at & 15u;
+        uint32_t w[4 * U + 4];                                  // own words, then the next lane's first unit
+#pragma unroll
+        for (int k = 0; k < 4 * U; ++k) w[k] = x.w[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[4 * U + k] = __shfl_down_sync(0xffffffffu, x.w[k], 1);
+        const int lane = threadIdx.x & 31;
+        if (off == 0u) {
+            if (n + 8 <= N) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    reinterpret_cast<uint4*>(at)[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (n + j < N) put_element(row + n + j, x, j);
+            }
+            return;
+        }
+        // aligned units from 16 - off bytes into the own elements on; the
+        // last one ends with the next lane's first `head` elements
+        const int head = (int)((16u - off) / sizeof(T));
+        uint4* to = reinterpret_cast<uint4*>(at + 16u - off);
+        const bool join = lane < 31 && n + 8 + head <= N;
+        if constexpr (U == 2) {
+            if (n + 8 <= N) to[0] = shifted<0>(w, 16u - off);
+        }
+        if (join) to[U - 1] = shifted<4 * U - 4>(w, 16u - off);
+        // what no unit covers: the head where the lane before has not joined
+        // it, the rest where this lane has not joined
+        const bool own_head = lane == 0 || n + head > N;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (FIRST) ss = fmaf(f[j], f[j], ss);
-            f[j] *= g[j];
+            const int per = (int)(16 / sizeof(T));              // elements of a unit
+            const bool in_head = j < head;
+            const bool in_first = U == 2 && !in_head && j < head + per && n + 8 <= N;
+            const bool covered = in_head ? !own_head : (in_first || join);
+            if (!covered && n + j < N) put_element(row + n + j, x, j);
         }
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void quant_codes(const QuantArgs& p, int64_t t, int i, int tpr, const float (&f)[8],
-                                            float pre, float inv) {
-    int8_t* row = p.q + t * p.ldq;
-    int c[8];
+// Two elements as fp32.
+__device__ __forceinline__ uint64_t widen(const Raw<__half>& x, int k) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x.w[k]));
+    return pair(f.x, f.y);
+}
+__device__ __forceinline__ uint64_t widen(const Raw<__nv_bfloat16>& x, int k) {
+    return pair(__uint_as_float(x.w[k] << 16), __uint_as_float(x.w[k] & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t widen(const Raw<float>& x, int k) {
+    return pair(__uint_as_float(x.w[2 * k]), __uint_as_float(x.w[2 * k + 1]));
+}
+
+// h + delta rounded once to h's type: the norm and every later reader of the
+// stream see the same h'.  (The 16-bit additions round the exact sum.)
+__device__ __forceinline__ void add_delta(Raw<__half>& h, const Raw<__half>& d) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = max(-127, min(127, __float2int_rn(f[j] * pre * inv)));
-    if constexpr (VEC) {
-        const int n = quant_index<true>(i, 0, tpr);
-        uint32_t w[2];
+    for (int k = 0; k < 4; ++k) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(h.w[k]) : "r"(d.w[k]));
+}
+__device__ __forceinline__ void add_delta(Raw<__nv_bfloat16>& h, const Raw<__nv_bfloat16>& d) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            w[k] = (uint32_t)(c[4 * k] & 255) | ((uint32_t)(c[4 * k + 1] & 255) << 8) |
-                   ((uint32_t)(c[4 * k + 2] & 255) << 16) | ((uint32_t)(c[4 * k + 3] & 255) << 24);
-        if (n < p.N) *reinterpret_cast<uint2*>(row + n) = make_uint2(w[0], w[1]);
+    for (int k = 0; k < 4; ++k) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(h.w[k]) : "r"(d.w[k]));
+}
+template <typename E>
+__device__ __forceinline__ void add_delta(Raw<float>& h, const Raw<E>& d) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = unpair(add2(widen(h, k), widen(d, k)));
+        h.w[2 * k] = __float_as_uint(f.x);
+        h.w[2 * k + 1] = __float_as_uint(f.y);
+    }
+}
+
+__device__ __forceinline__ float silu(float g) {
+    // 2^(-g log2 e) overflows to infinity below g = -88 and its reciprocal is
+    // then 0: silu's own limit.  The approximate exponential and reciprocal are
+    // within a few 2^-23 of the value, far below half a step of 8 bits;
+    // flushing their subnormals saves the instructions that would scale them.
+    float e, rc;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + e));
+    return g * rc;
+}
+
+// A chunk's inputs.
+template <int KIND, typename E, typename H>
+struct QuantIn {
+    Raw<H> a;
+    Raw<E> b;
+};
+
+template <int KIND, typename E, typename H, bool VEC>
+__device__ __forceinline__ void quant_inputs(const QuantArgs& p, int64_t t, int n, QuantIn<KIND, E, H>& x) {
+    x.a = quant_load<VEC>(static_cast<const H*>(p.a) + t * p.lda, n, p.N);
+    if (KIND == kQuantSilu || (KIND == kQuantNorm && p.b))
+        x.b = quant_load<VEC>(static_cast<const E*>(p.b) + t * p.ldb, n, p.N);
+}
+
+// The row's values before its common factor; their largest magnitude, and for
+// rmsnorm h' (written) and the sum of its squares.
+template <int KIND, typename E, typename H, bool VEC>
+__device__ __forceinline__ void quant_values(const QuantArgs& p, int64_t t, int n, QuantIn<KIND, E, H>& x,
+                                             uint64_t (&v)[4], uint64_t& ss, float& mx) {
+    if constexpr (KIND == kQuantNorm) {
+        const Raw<E> g = quant_load<VEC>(static_cast<const E*>(p.gamma), n, p.N);
+        if (p.b) add_delta(x.a, x.b);
+        if (p.h_out) quant_store<VEC>(static_cast<H*>(p.h_out) + t * p.ldo, n, p.N, x.a);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t h = widen(x.a, k);
+            ss = fma2(h, h, ss);
+            v[k] = mul2(h, widen(g, k));
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int n = quant_index<false>(i, j, tpr);
-            if (n < p.N) row[n] = (int8_t)c[j];
+        for (int k = 0; k < 4; ++k) {
+            v[k] = widen(x.a, k);
+            if constexpr (KIND == kQuantSilu) {
+                const float2 g = unpair(v[k]);
+                v[k] = mul2(pair(silu(g.x), silu(g.y)), widen(x.b, k));
+            }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = max_abs(mx, v[k]);
+}
+
+// Codes of a chunk: v * pre * inv is at most 127 (1 + 2^-22) in magnitude, so
+// adding 1.5 * 2^23 rounds it to the nearest integer (ties to even) and leaves
+// that integer, modulo 2^8, in the low byte.  (The addition is a scalar one:
+// a paired multiplication and a paired addition were seen to be contracted
+// into one rounding, which moves ties.)
+__device__ __forceinline__ void quant_codes(const QuantArgs& p, int64_t t, int n, uint64_t (&v)[4], float pre,
+                                            float inv, bool finite) {
+    const uint64_t inv2 = pair(inv, inv);
+    constexpr float kMagic = 12582912.f;
+    if (pre != 1.f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], pair(pre, pre));
+    }
+    uint32_t c[4];   // two codes each, in the low bytes
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = unpair(mul2(v[k], inv2));
+        c[k] = __byte_perm(__float_as_uint(__fadd_rn(f.x, kMagic)), __float_as_uint(__fadd_rn(f.y, kMagic)), 0x0040);
+    }
+    uint32_t w[2] = {__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410)};
+    if (!finite) w[0] = w[1] = 0u;   // a NaN or an infinity has no code
+    int8_t* at = p.q + t * p.ldq + n;
+    if (n + 8 <= p.N) {
+        *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (n + j < p.N) at[j] = (int8_t)(w[j / 4] >> (8 * (j % 4)));
     }
 }
 
-// blockDim = (threads of a row, rows of the CTA); threads of a row a multiple of 32.
+// Threads that a CTA of the kernel with VPT chunks a thread may have (what its
+// registers allow).
+__host__ __device__ constexpr int quant_max_threads(int vpt) { return vpt <= 1 ? 1024 : vpt == 2 ? 768 : 512; }
+
+constexpr int kQuantMaxParts = 8;   // a portable cluster: 8 * 512 threads * 4 * 8 elements hold the longest row
+
+// blockDim = (threads of a row, rows of the CTA); threads of a row a multiple
+// of 32; one row per cluster where p.parts > 1.
 template <int KIND, typename E, typename H, int VPT, bool VEC>
-__global__ void fluxbin_quant_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(quant_max_threads(VPT)) fluxbin_quant_kernel(const QuantArgs p) {
     __shared__ float s_sum[32];
     __shared__ unsigned int s_max[32];
-    const int tpr = (int)blockDim.x;
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    __shared__ float s_part_sum[kQuantMaxParts];
+    __shared__ unsigned int s_part_max[kQuantMaxParts];
+    const int tpr = (int)blockDim.x, parts = p.parts;
+    const int rank = (int)(blockIdx.x % (unsigned)parts);
+    const int64_t t = (int64_t)(blockIdx.x / (unsigned)parts) * blockDim.y + threadIdx.y;
+    const int n0 = (rank * VPT * tpr + (int)threadIdx.x) * 8;   // chunk i at n0 + 8 i tpr
     asm volatile("griddepcontrol.launch_dependents;");
+    // the others of the cluster have started once this barrier is passed (below)
+    if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool live = t < p.T;
 
-    float ss = 0.f;
-    unsigned int mx = 0u;
-    float f[VPT ? VPT : 1][8];
-    const int chunks = (p.N + 8 * tpr - 1) / (8 * tpr);
+    uint64_t ss2 = 0ull;
+    float mxf = 0.f;
+    uint64_t v[VPT][4];
     if (live) {
-        if constexpr (VPT > 0) {
+        // every load before the first store
+        QuantIn<KIND, E, H> x[VPT];
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                quant_values<KIND, E, H, VEC, true>(p, t, i, tpr, f[i], ss);
+        for (int i = 0; i < VPT; ++i) quant_inputs<KIND, E, H, VEC>(p, t, n0 + 8 * i * tpr, x[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx = max(mx, __float_as_uint(f[i][j]) & 0x7fffffffu);
-            }
-        } else {
-            for (int i = 0; i < chunks; ++i) {
-                quant_values<KIND, E, H, VEC, true>(p, t, i, tpr, f[0], ss);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) mx = max(mx, __float_as_uint(f[0][j]) & 0x7fffffffu);
-            }
-        }
+        for (int i = 0; i < VPT; ++i) quant_values<KIND, E, H, VEC>(p, t, n0 + 8 * i * tpr, x[i], v[i], ss2, mxf);
     }
-    // the row's maximum and sum: within the warps, then over the row's warps
-    // (the same order in every thread)
-    mx = __reduce_max_sync(0xffffffffu, mx);
+    float ss = unpair(ss2).x + unpair(ss2).y;
+    // the row's maximum and sum: within the warps, over the CTA's warps, over
+    // the cluster's CTAs (the same order in every thread)
+    unsigned int mx = __reduce_max_sync(0xffffffffu, __float_as_uint(mxf) & 0x7fffffffu);
     if constexpr (KIND == kQuantNorm) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    const int wpr = tpr / 32;
+    const int wpr = tpr / 32, lane = threadIdx.x & 31;
     if (wpr > 1) {
-        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, w0 = (int)threadIdx.y * wpr;
+        const int w = threadIdx.x >> 5, w0 = (int)threadIdx.y * wpr;
         if (lane == 0) {
             s_max[w0 + w] = mx;
             s_sum[w0 + w] = ss;
@@ -227,6 +402,24 @@ __global__ void fluxbin_quant_kernel(const QuantArgs p) {
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         }
     }
+    if (parts > 1) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if ((int)threadIdx.x < parts) {
+            uint32_t am, as;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                : "=r"(am) : "r"((uint32_t)__cvta_generic_to_shared(s_part_max + rank)), "r"((int)threadIdx.x));
+            asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                : "=r"(as) : "r"((uint32_t)__cvta_generic_to_shared(s_part_sum + rank)), "r"((int)threadIdx.x));
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(am), "r"(mx) : "memory");
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(as), "r"(__float_as_uint(ss)) : "memory");
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        ss = 0.f;
+        for (int r = 0; r < parts; ++r) {
+            mx = max(mx, s_part_max[r]);
+            ss += s_part_sum[r];
+        }
+    }
     if (!live) return;
     const float amax = __uint_as_float(mx);
     float factor = 1.f;
@@ -237,29 +430,12 @@ __global__ void fluxbin_quant_kernel(const QuantArgs p) {
     float s = amax * factor / 127.f;
     const bool finite = fabsf(s) < INFINITY;
     if (!finite) s = NAN;
-    if (threadIdx.x == 0) p.scale[t] = s;
+    if (threadIdx.x == 0 && rank == 0) p.scale[t] = s;
     // 127 / amax, the row scaled up first where the quotient would overflow
     const float pre = amax < 0x1p-100f ? 0x1p100f : 1.f;
     const float inv = (finite && mx != 0u) ? 127.f / (amax * pre) : 0.f;
-    if constexpr (VPT > 0) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (!finite) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[i][j] = 0.f;   // a NaN or infinite value has no code
-            }
-            quant_codes<VEC>(p, t, i, tpr, f[i], pre, inv);
-        }
-    } else {
-        for (int i = 0; i < chunks; ++i) {
-            quant_values<KIND, E, H, VEC, false>(p, t, i, tpr, f[0], ss);
-            if (!finite) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[0][j] = 0.f;
-            }
-            quant_codes<VEC>(p, t, i, tpr, f[0], pre, inv);
-        }
-    }
+    for (int i = 0; i < VPT; ++i) quant_codes(p, t, n0 + 8 * i * tpr, v[i], pre, inv, finite);
 }
 
 }  // namespace fluxbin
