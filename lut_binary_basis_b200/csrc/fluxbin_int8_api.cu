@@ -65,6 +65,9 @@ int launch(K kernel, dim3 grid, dim3 block, size_t smem, int cluster, void* stre
 
 using QuantFn = void (*)(QuantArgs);
 
+constexpr int64_t kQuantFewBlocks = 148;                 // CTAs that have an SM each
+constexpr int64_t kQuantManyVecs = (int64_t)1 << 20;     // of 8 elements: 8 million elements
+
 template <int KIND, typename E, typename H, bool VEC>
 QuantFn pick_quant(int vpt) {
     switch (vpt) {
@@ -117,10 +120,24 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     a.eps = eps;
     const bool vec = N % 8 == 0 && in0.rows_aligned16() && (!in1.p || in1.rows_aligned16()) &&
                      (!gamma || ptr_aligned(gamma, 16)) && (!h_out.p || h_out.rows_aligned16());
+    // Vectors of 8 elements a thread, and CTAs a row (B200, us a call, a graph
+    // of calls).  Few rows: one vector, and a cluster once it leaves a CTA 256
+    // threads or more (gate 1x11008: four CTAs 2.2, one with two vectors 2.6;
+    // norm 1x4096: one CTA 2.1, two 2.5).  Many rows: four vectors, so that
+    // several CTAs of an SM are in different phases (quant 4096x8192 1 / 2 / 4
+    // vectors 31 / 22 / 19.6, norm 2048x8192 27.4 / 22.4 / 21.0), but two for
+    // the gate, a 32-bit stream and unaligned rows, which need more registers
+    // (gate 2048x11008 24.3 / 26.8, norm of a 32-bit 2048x8192 32.3 / 32.8).
     const int64_t vecs = (N + 7) / 8;
-    int vpt = 1;
-    while (vpt < 4 && vecs > (int64_t)vpt * quant_max_threads(vpt)) vpt *= 2;
-    int parts = 1;
+    int vpt = 1, parts = 1;
+    if (vecs >= 1024 && T * (vecs > 2048 ? 8 : 4) <= kQuantFewBlocks) {
+        parts = vecs > 2048 ? 8 : 4;
+    } else if (T * vecs >= kQuantManyVecs) {
+        vpt = vecs < 512 ? 1 : (KIND == kQuantSilu || h32 || !vec) ? 2 : 4;
+    } else if (T > kQuantFewBlocks / 4 && vecs >= 512) {
+        vpt = 2;
+    }
+    while (vpt < 4 && vecs > (int64_t)parts * vpt * quant_max_threads(vpt)) vpt *= 2;
     while (vecs > (int64_t)parts * vpt * quant_max_threads(vpt)) parts *= 2;
     const int64_t per_thread = (int64_t)parts * vpt;
     const int tpr = std::max(32, (int)(((vecs + per_thread - 1) / per_thread + 31) / 32 * 32));
