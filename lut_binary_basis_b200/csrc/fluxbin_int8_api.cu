@@ -11,6 +11,7 @@
 #include "../../include/fluxbin.h"
 #include "fluxbin_device.h"
 #include "fluxbin_int8.cuh"
+#include "fluxbin_int8_mv.cuh"
 #include "fluxbin_int8_tc.cuh"
 #include "fluxbin_int8_tc2.cuh"
 #include "fluxbin_quant.cuh"
@@ -168,6 +169,7 @@ std::mutex g_int8_mu;
 
 struct Int8Device {
     bool ready = false;
+    int index = 0;
     int sm_count = 0;
     unsigned int* err = nullptr;
 } g_int8_dev[kMaxDevices];
@@ -192,6 +194,11 @@ Int8PairFn pick_pair(bool acc) { return acc ? &fluxbin_int8_pair_kernel<Y, true>
 Int8PairFn pick_int8_pair(uint32_t flags) {
     const bool acc = (flags & kInt8Accumulate) != 0;
     return (flags & kInt8YFp32) ? pick_pair<float>(acc) : (flags & kInt8Bf16) ? pick_pair<__nv_bfloat16>(acc) : pick_pair<__half>(acc);
+}
+template <typename Y>
+Int8EmptyFn pick_mv(bool acc, bool two) {
+    return two ? (acc ? &fluxbin_int8_mv_kernel<Y, true, 2> : &fluxbin_int8_mv_kernel<Y, false, 2>)
+               : (acc ? &fluxbin_int8_mv_kernel<Y, true, 1> : &fluxbin_int8_mv_kernel<Y, false, 1>);
 }
 template <typename Y>
 Int8EmptyFn pick_empty(bool acc) { return acc ? &fluxbin_int8_empty_kernel<Y, true> : &fluxbin_int8_empty_kernel<Y, false>; }
@@ -227,6 +234,7 @@ int int8_device(Int8Device* out) {
                     return report_cuda_failure(e);
         const int st = device_error_word(dev, &d.err);
         if (st != FLUXBIN_OK) return st;
+        d.index = dev;
         d.ready = true;
     }
     *out = d;
@@ -264,6 +272,32 @@ int encode_y(CUtensorMap* map, const Int8Args& p, int box, int32_t* bulk) {
     return r == CUDA_SUCCESS ? FLUXBIN_OK : report_cuda_failure(cudaErrorInvalidValue);
 }
 
+// How many clusters of `splits` CTAs, one CTA per SM, the device holds at
+// once.  (A cluster sits inside one of the GPU's processing clusters, whose
+// sizes differ.  B200: 74 of 2, 45 of 3, 33 of 4, 26 of 5, 22 of 6, 15 of 7 and 8.)
+int resident_clusters(const Int8Device& d, int splits) {
+    static int known[kMaxDevices][kI8MaxSplits + 1];
+    std::lock_guard<std::mutex> lock(g_int8_mu);
+    int& n = known[d.index][splits];
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)splits);
+    cfg.blockDim = dim3(kI8Threads);
+    cfg.dynamicSmemBytes = (size_t)kI8MaxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, pick_int8_tc(0), &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+    }
+    return n;
+}
+
 // Tiles, split and ring of a call; returns the number of tiles.
 //
 // A tile's K is split until the CTAs fill one wave of the GPU, never more
@@ -274,7 +308,7 @@ int encode_y(CUtensorMap* map, const Int8Args& p, int box, int32_t* bulk) {
 // against 11.4), unless its 148 slots would stay a quarter empty
 // (128x11008x4096, 86 tiles: 3 splits on two CTAs per SM 14.6, none on one
 // 16.2).  One CTA per SM is enough where a CTA's share is down to 8 stages
-// (1x4096x4096 with 4 splits 7.4, with 8 7.6; 1x4096x11008 12.8 and 11.7).
+// (16x4096x4096 with 4 splits 7.4, with 8 7.6; 16x4096x11008 12.8 and 11.7).
 int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
     Int8TcArgs& a = *out;
     a.kblocks = (p.N + kI8K - 1) / kI8K;
@@ -287,13 +321,18 @@ int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
     const bool whole = a.bn > 192 || (a.bn > 112 && one * tiles * 4 >= 3 * d.sm_count);
     int splits = whole || (one >= 1 && a.kblocks <= 8 * one) ? one : two;
     splits = std::max(1, std::min(splits, a.kblocks / 2));
-    a.splits = splits;
-    const int smem = whole ? kI8MaxSmem : 112 * 1024;
     const int stage = int8_stage_bytes(a.bn);
-    const int per_cta = a.kblocks / splits + 1;
-    a.stages = std::max(2, std::min(std::min(kI8MaxStages, per_cta), (smem - kI8RingOff) / stage));
-    // the ring holds the tile's partial sums, or its y, at the end
-    a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
+    for (;; --splits) {
+        a.splits = splits;
+        const int per_cta = a.kblocks / splits + 1;
+        const int room = ((whole ? kI8MaxSmem : 112 * 1024) - kI8RingOff) / stage;
+        a.stages = std::max(2, std::min(std::min(kI8MaxStages, per_cta), room));
+        // the ring holds the tile's partial sums, or its y, at the end
+        a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
+        // (32x6144x4096, 48 tiles: 4 and 5 splits 8.6 and 9.1 us, 6, which do not
+        // all fit, 15.0)
+        if (splits == 1 || resident_clusters(d, splits) * (whole ? 1 : 2) >= tiles) break;
+    }
     return tiles;
 }
 
@@ -347,6 +386,15 @@ int run_pairs(const Int8Args& p, const Int8Device& d, void* stream) {
                   stream, mw, mx, my, a);
 }
 
+// The register kernel: layers that one wave holds (B200, us a call, register /
+// ring kernel: 1x4096x4096 3.8 / 6.8, 8x8192x4096 7.8 / 9.1, 16x4096x4096 5.3 /
+// 7.1; 8x11008x4096 10.8 / 10.5, 16x8192x4096 10.0 / 9.2, 1x28672x8192 39.3 /
+// 37.8).
+bool use_mv(const Int8Args& p) {
+    if (p.flags & FLUXBIN_FLAG_TEST_WAIT_TIMEOUT) return false;   // it has no waits
+    return p.T <= 2 * kMvTokens && (int64_t)p.M * p.N <= ((int64_t)1 << (p.T <= kMvTokens ? 25 : 24));
+}
+
 int run_int8(const Int8Args& p, void* stream) {
     const bool acc = (p.flags & kInt8Accumulate) != 0;
     if (p.N == 0) {
@@ -355,6 +403,12 @@ int run_int8(const Int8Args& p, void* stream) {
         Int8EmptyFn fn = (p.flags & kInt8YFp32) ? pick_empty<float>(acc)
                          : (p.flags & kInt8Bf16) ? pick_empty<__nv_bfloat16>(acc) : pick_empty<__half>(acc);
         return launch(fn, dim3((unsigned)blocks), dim3(256), 0, 1, stream, p);
+    }
+    if (use_mv(p)) {
+        const bool two = p.T > kMvTokens;
+        Int8EmptyFn fn = (p.flags & kInt8YFp32) ? pick_mv<float>(acc, two)
+                         : (p.flags & kInt8Bf16) ? pick_mv<__nv_bfloat16>(acc, two) : pick_mv<__half>(acc, two);
+        return launch(fn, dim3((unsigned)((p.M + (int64_t)kMvRows - 1) / kMvRows)), dim3(32 * kMvWarps), 0, 1, stream, p);
     }
     Int8Device d;
     int st = int8_device(&d);
