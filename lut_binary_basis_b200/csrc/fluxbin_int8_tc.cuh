@@ -164,6 +164,37 @@ __device__ __forceinline__ int4 add4(const int4& a, const int4& b) {
     return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
+// Tokens c, c + 8, .. below c1 of a split tile: the sums of `splits` <= MAX
+// CTAs, U tokens at a time, scaled and written.
+template <typename Y, bool ACC, int MAX, int U>
+__device__ __forceinline__ void int8_sum_split(const Int8Args& p, uint32_t ring, int splits, int64_t t0, int c, int c1,
+                                               int m0, int mq, const float (&sw4)[4], int failed) {
+    constexpr int kWarps = kI8Threads / 32;
+    uint32_t peer[MAX];
+#pragma unroll
+    for (int r = 0; r < MAX; ++r) peer[r] = dsmem_addr(ring + (uint32_t)(mq * 4), r < splits ? r : 0);
+    for (; c < c1; c += U * kWarps) {
+        int4 part[U][MAX];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < MAX; ++r)
+                if (r < splits && c + u * kWarps < c1)
+                    part[u][r] = ld_dsmem4(peer[r] + (uint32_t)((c + u * kWarps) * kI8Rows * 4));
+        const bool ok = !__any_sync(0xffffffffu, failed != 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int cu = c + u * kWarps;
+            if (cu >= c1 || m0 + mq >= p.M) continue;
+            int4 v = part[u][0];
+#pragma unroll
+            for (int r = 1; r < MAX; ++r)
+                if (r < splits) v = add4(v, part[u][r]);
+            int8_store4<Y, ACC>(p, t0 + cu, m0 + mq, smem_at<const float>((uint32_t)(kI8SxOff + 4 * cu)), sw4, v, ok);
+        }
+    }
+}
+
 template <typename Y, bool ACC>
 __global__ void __launch_bounds__(kI8Threads)
     fluxbin_int8_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -358,36 +389,16 @@ __global__ void __launch_bounds__(kI8Threads)
     }
     if (a.splits > 1) {
         int8_cluster_sync();
+        // one lane asks each CTA whether it failed, while the sums are on their way
+        const int failed = lane < a.splits ? ld_dsmem(dsmem_addr(sb + kFailed, lane)) : 0;
         // this CTA's share of the tile's tokens, added over the cluster: a
-        // warp has the 128 channels of a token, four a lane
-        bool all_ok = true;
-        for (int r = 0; r < a.splits; ++r) all_ok = all_ok && ld_dsmem(dsmem_addr(sb + kFailed, r)) == 0;
-        uint32_t peer[kI8MaxSplits];
-#pragma unroll
-        for (int r = 0; r < kI8MaxSplits; ++r) peer[r] = dsmem_addr(ring + (uint32_t)(mq * 4), r < a.splits ? r : 0);
+        // warp has the 128 channels of a token, four a lane, and the loads of
+        // several tokens overlap
         const int c0 = nt * rank / a.splits, c1 = nt * (rank + 1) / a.splits;
-        for (int c = c0 + warp; c < c1; c += 2 * (kI8Threads / 32)) {
-            // two tokens at a time: their loads overlap
-            const int cb = c + kI8Threads / 32;
-            int4 part[2][kI8MaxSplits];
-#pragma unroll
-            for (int r = 0; r < kI8MaxSplits; ++r)
-                if (r < a.splits) {
-                    part[0][r] = ld_dsmem4(peer[r] + (uint32_t)(c * kI8Rows * 4));
-                    if (cb < c1) part[1][r] = ld_dsmem4(peer[r] + (uint32_t)(cb * kI8Rows * 4));
-                }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int ch = h ? cb : c;
-                if (ch >= c1 || m0 + mq >= p.M) continue;
-                int4 v = part[h][0];
-#pragma unroll
-                for (int r = 1; r < kI8MaxSplits; ++r)
-                    if (r < a.splits) v = add4(v, part[h][r]);
-                int8_store4<Y, ACC>(p, t0 + ch, m0 + mq, smem_at<const float>((uint32_t)(kI8SxOff + 4 * ch)), sw4, v,
-                                    all_ok);
-            }
-        }
+        if (a.splits <= 4)
+            int8_sum_split<Y, ACC, 4, 2>(p, ring, a.splits, t0, c0 + warp, c1, m0, mq, sw4, failed);
+        else
+            int8_sum_split<Y, ACC, kI8MaxSplits, 2>(p, ring, a.splits, t0, c0 + warp, c1, m0, mq, sw4, failed);
         int8_cluster_sync();                     // the others have read this CTA's sums
     }
 }
