@@ -399,7 +399,9 @@ __global__ void __launch_bounds__(kI8Threads)
             int8_sum_split<Y, ACC, 4, 2>(p, ring, a.splits, t0, c0 + warp, c1, m0, mq, sw4, failed);
         else
             int8_sum_split<Y, ACC, kI8MaxSplits, 2>(p, ring, a.splits, t0, c0 + warp, c1, m0, mq, sw4, failed);
-        int8_cluster_sync();                     // the others have read this CTA's sums
+        // the others have read this CTA's sums (nothing to publish: a release
+        // would wait for the stores of y)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     }
 }
 
