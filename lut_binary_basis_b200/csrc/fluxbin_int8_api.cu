@@ -380,7 +380,7 @@ int run_pairs(const Int8Args& p, const Int8Device& d, void* stream) {
     if ((st = encode_rows(&mw, p.w, p.M, p.N, p.ldw, kI8Rows)) != FLUXBIN_OK) return st;
     if ((st = encode_rows(&mx, p.x, p.T, p.N, p.ldx, a.bn / 2)) != FLUXBIN_OK) return st;
     CUtensorMap my = mx;
-    if ((st = encode_y(&my, p, kI8PairChunk, &a.bulk)) != FLUXBIN_OK) return st;
+    if ((st = encode_y(&my, p, int8_pair_chunk((p.flags & kInt8YFp32) ? 4 : 2), &a.bulk)) != FLUXBIN_OK) return st;
     const int64_t pairs = std::min<int64_t>(a.tiles, d.sm_count / 2);
     return launch(pick_int8_pair(p.flags), dim3((unsigned)(2 * pairs)), dim3(kI8PairThreads), (size_t)kI8PairSmem, 1,
                   stream, mw, mx, my, a);

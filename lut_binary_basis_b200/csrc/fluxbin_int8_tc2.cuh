@@ -9,13 +9,17 @@
 // from L2, more than one SM takes in; the pair's asks for 64.
 //
 // The grid is persistent (one pair per two SMs) and each CTA holds two
-// accumulators in tensor memory: four warps empty one into y while the matrix
+// accumulators in tensor memory: eight warps empty one into y while the matrix
 // instructions of the next tile run into the other.
 //
 // Roles per CTA: warp 0 copies (TMA, both CTAs signal the leader's full
 // barriers), warp 1 of the leader issues the matrix instructions and commits
-// them to both CTAs' empty barriers, warps 2-5 write the outputs (channels lie
-// along the lanes: a warp stores 32 consecutive channels of a token).
+// them to both CTAs' empty barriers, warps 2-5 and 6-9 write the outputs, chunk
+// by chunk in turn: scaled and rounded into a staging buffer of [tokens][128
+// channels] and from there to y by TMA.  (An SM gets a store away every 13 to
+// 20 clocks, however narrow it is: 32 channels of a token at a time, straight
+// from the registers, left the last tile's outputs exposed for 17 us.)  Rows of
+// y that TMA cannot write go out of the buffer in the widest stores they allow.
 // Tiles run token tile by token tile within groups of 8 token tiles, so that
 // the pairs at work share their weights and a group's tokens through L2.
 //
@@ -28,7 +32,7 @@
 
 namespace fluxbin {
 
-constexpr int kI8PairThreads = 192;
+constexpr int kI8PairThreads = 320;
 constexpr int kI8PairStages = 6;
 constexpr int kI8PairGroup = 8;          // token tiles that share a pass over the weights
 
@@ -43,13 +47,13 @@ struct Int8PairArgs {
 };
 
 __host__ __device__ constexpr int int8_pair_stage_bytes(int bn) { return kI8Rows * kI8K + (bn / 2) * kI8K; }
-// Always sized for the widest tile and y: all of an SM's shared memory.
-constexpr int kI8PairChunk = 32;         // tokens staged at a time
+// Always sized for the widest tile: all of an SM's shared memory.
 constexpr int kI8PairRingOff = 1024;
 constexpr int kI8PairOutOff = kI8PairRingOff + kI8PairStages * int8_pair_stage_bytes(kI8MaxBn);
-constexpr int kI8PairOutBytes = kI8PairChunk * kI8Rows * 4;        // one of two staging buffers
-constexpr int kI8PairSxOff = kI8PairOutOff + 2 * kI8PairOutBytes;  // [2][256] token scales
+constexpr int kI8PairOutBytes = 8192;    // a staging buffer: 32 tokens of a 16-bit y, 16 of a 32-bit one
+constexpr int kI8PairSxOff = kI8PairOutOff + 4 * kI8PairOutBytes;  // [2][256] token scales
 constexpr int kI8PairSmem = kI8PairSxOff + 2 * kI8MaxBn * 4;
+__host__ __device__ constexpr int int8_pair_chunk(int size) { return kI8PairOutBytes / (kI8Rows * size); }
 
 __device__ __forceinline__ void int8_pair_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
     asm volatile(
@@ -86,16 +90,47 @@ __device__ __forceinline__ void int8_ld32(uint32_t taddr, int (&v)[32]) {
         : "r"(taddr));
 }
 
-// The four output warps.
-__device__ __forceinline__ void int8_out_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The four output warps of a group, or both groups.
+__device__ __forceinline__ void int8_out_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+__device__ __forceinline__ void int8_out_sync_all() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
-// Requests chunk q of a tile's y (accumulation) into its staging buffer.
-__device__ __forceinline__ void int8_pair_load_y(const CUtensorMap& map_y, uint32_t sb, int m0, int64_t t0, int q,
-                                                 uint32_t y_full0, int size) {
-    const int buf = q & 1;
-    int8_expect(y_full0 + 8 * buf, (uint32_t)(kI8PairChunk * kI8Rows * size));
-    int8_tma(sb + (uint32_t)(kI8PairOutOff + buf * kI8PairOutBytes), &map_y, m0, (int)t0 + q * kI8PairChunk,
-             y_full0 + 8 * buf);
+// C columns of the accumulators.
+template <int C>
+__device__ __forceinline__ void int8_ld(uint32_t taddr, int (&v)[C]) {
+    if constexpr (C == 32) int8_ld32(taddr, v);
+    else int8_ld16(taddr, v);
+}
+
+// Rows of y (tokens t0 .., channels m0 ..) to or from a staging buffer, by the
+// 128 threads of a group: a warp per row, four channels a lane where the rows
+// allow it.
+template <typename Y, int C, bool OUT>
+__device__ __forceinline__ void int8_copy_rows(const Int8Args& p, uint32_t buf, int64_t t0, int m0, int e) {
+    const int lane = e & 31;
+    struct alignas(4 * sizeof(Y)) Quad { Y v[4]; };
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) {
+        const int j = (e >> 5) + 4 * i;
+        if (t0 + j >= p.T) continue;
+        Y* y = static_cast<Y*>(p.y) + (t0 + j) * p.ldy + m0;
+        const uint32_t row = buf + (uint32_t)(j * kI8Rows * (int)sizeof(Y));
+        if (p.vec4 && m0 + 4 * lane + 4 <= p.M) {
+            Quad& o = smem_at<Quad>(row + (uint32_t)(4 * lane * (int)sizeof(Y)));
+            if (OUT) *reinterpret_cast<Quad*>(y + 4 * lane) = o;
+            else o = *reinterpret_cast<const Quad*>(y + 4 * lane);
+        } else {
+            // (with four channels a lane only the row's ragged end)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int ch = p.vec4 ? 4 * lane + k : lane + 32 * k;
+                if (m0 + ch < p.M) {
+                    Y& o = smem_at<Y>(row + (uint32_t)(ch * (int)sizeof(Y)));
+                    if (OUT) y[ch] = o;
+                    else o = y[ch];
+                }
+            }
+        }
+    }
 }
 
 struct Int8PairTile {
@@ -119,8 +154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
     const uint32_t sb = smem_base();
     // barriers: full and empty per stage, accumulator full and empty (2), done
     const uint32_t full0 = sb, empty0 = sb + 64, acc_full0 = sb + 128, acc_empty0 = sb + 144, done = sb + 160,
-                   y_full0 = sb + 168;
-    constexpr uint32_t kSlot = 184, kDrained = 188;
+                   y_full0 = sb + 168;             // (four, one per staging buffer)
+    constexpr uint32_t kSlot = 200, kDrained = 204;
     const uint32_t ring = sb + kI8PairRingOff;
     const uint32_t stage_bytes = (uint32_t)int8_pair_stage_bytes(a.bn);
     const int rank = (int)(blockIdx.x & 1);
@@ -138,9 +173,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc_mbar_init(acc_full0 + 8 * b, 1);
-            tc_mbar_init(acc_empty0 + 8 * b, 8);   // four warps of each CTA
-            tc_mbar_init(y_full0 + 8 * b, 1);
+            tc_mbar_init(acc_empty0 + 8 * b, 16);  // eight warps of each CTA
         }
+        for (int b = 0; b < 4; ++b) tc_mbar_init(y_full0 + 8 * b, 1);
         tc_mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -230,57 +265,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
     } else {
         // ---- outputs ----
         asm volatile("griddepcontrol.wait;" ::: "memory");
+        constexpr int C = int8_pair_chunk((int)sizeof(Y));   // tokens of a chunk
+        const int group = (warp - 2) >> 2;         // takes every other chunk
         const int quarter = warp & 3;              // the lanes of tensor memory that this warp reaches
-        const int e = tid - 64, row = quarter * 32 + lane;
-        const int chunks = a.bn / kI8PairChunk;
-        uint32_t y_parity = 0u;                    // of the loads of y into each staging buffer (one bit each)
+        const int e = (tid - 64) & 127, row = quarter * 32 + lane;
+        const int chunks = a.bn / C;
+        // the group's two staging buffers
+        const uint32_t buf0 = (uint32_t)(kI8PairOutOff + 2 * group * kI8PairOutBytes), y_full = y_full0 + 16 * group;
+        uint32_t y_parity = 0u;                    // of the loads of y into each of them (one bit each)
         int64_t n = 0;
         for (int64_t i = first; i < a.tiles; i += step, ++n) {
             const Int8PairTile t = int8_pair_tile(a, i);
             const int b = (int)(n & 1);
             const int m0 = (t.tm * 2 + rank) * kI8Rows, m = m0 + row;
             const int64_t t0 = (int64_t)t.tt * a.bn;
-            // the tile's scales, requested before the accumulators are ready
-            const float sw = m < p.M ? __ldg(p.sw + m) : 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = h * 128 + e;
-                smem_at<float>(kI8PairSxOff + (b * kI8MaxBn + c) * 4) = c < a.bn && t0 + c < p.T ? __ldg(p.sx + t0 + c) : 0.f;
-            }
             // TMA writes whole 16-byte pieces: a ragged last tile only where
             // M ends on one
             const bool bulk = a.bulk > (m0 + kI8Rows <= p.M ? 0 : 1);
-            if (ACC && bulk && e == 0) {
+            // requests a chunk's y (accumulation) into its staging buffer
+            const auto load_y = [&](int q) {
+                const int k = (q >> 1) & 1;
+                int8_expect(y_full + 8 * k, (uint32_t)kI8PairOutBytes);
+                int8_tma(sb + buf0 + k * kI8PairOutBytes, &map_y, m0, (int)t0 + q * C, y_full + 8 * k);
+            };
+            // the tile's scales, requested before the accumulators are ready
+            const float sw = m < p.M ? __ldg(p.sw + m) : 0.f;
+            {
+                const int c = tid - 64;
+                smem_at<float>(kI8PairSxOff + (b * kI8MaxBn + c) * 4) = c < a.bn && t0 + c < p.T ? __ldg(p.sx + t0 + c) : 0.f;
+            }
+            if (ACC) {                             // (the tile before may have gone out by plain stores)
+                fence_async_smem();
+                int8_out_sync(group);
+            }
+            if (ACC && bulk && e == 0 && group < chunks) {
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                int8_pair_load_y(map_y, sb, m0, t0, 0, y_full0, (int)sizeof(Y));
+                load_y(group);
             }
             if (ok) ok = tc_mbar_wait(acc_full0 + 8 * b, (uint32_t)(n >> 1) & 1u, a.spin_limit);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            int8_out_sync();                       // the token scales are in place
+            int8_out_sync_all();                   // the token scales are in place
             const uint32_t acc = tmem + (uint32_t)(b * kI8MaxBn) + ((uint32_t)(quarter * 32) << 16);
-            for (int q = 0; q < chunks; ++q) {
-                const int buf = q & 1, c = q * kI8PairChunk;
-                const uint32_t out = (uint32_t)(kI8PairOutOff + buf * kI8PairOutBytes);
-                int v[32];
-                int8_ld32(acc + (uint32_t)c, v);
+            for (int q = group; q < chunks; q += 2) {
+                const int k = (q >> 1) & 1, c = q * C;
+                const uint32_t out = buf0 + (uint32_t)(k * kI8PairOutBytes);
+                int v[C];
+                int8_ld<C>(acc + (uint32_t)c, v);
+                // the staging buffer is free once what went out of it two
+                // chunks ago has been read; with accumulation the next chunk's
+                // y is requested a chunk ahead
                 if (bulk) {
-                    // the staging buffer is free once the copy out of it two
-                    // chunks ago has been read; with accumulation the next
-                    // chunk's y is requested a chunk ahead
                     if (e == 0) {
                         if (ACC) {
                             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                            if (q + 1 < chunks) int8_pair_load_y(map_y, sb, m0, t0, q + 1, y_full0, (int)sizeof(Y));
+                            if (q + 2 < chunks) load_y(q + 2);
                         } else {
                             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         }
                     }
-                    if (!ACC) int8_out_sync();
+                } else if (e == 0) {
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 }
-                float f[32];
+                if (!ACC || !bulk) int8_out_sync(group);
+                if (ACC && !bulk) {
+                    int8_copy_rows<Y, C, false>(p, out, t0 + c, m0, e);
+                    int8_out_sync(group);
+                }
+                float f[C];
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
+                for (int j = 0; j < C; j += 4) {
                     const float4 s4 = smem_at<const float4>(kI8PairSxOff + (b * kI8MaxBn + c + j) * 4);
                     f[j] = s4.x;
                     f[j + 1] = s4.y;
@@ -288,42 +342,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                     f[j + 3] = s4.w;
                 }
                 tc_wait_ld();
-                if (q == chunks - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) int8_remote_arrive(dsmem_addr(acc_empty0 + 8 * b, 0));
-                }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
+                for (int j = 0; j < C; ++j) {
                     f[j] = int8_value(v[j], f[j], sw);
                     if (!ok) f[j] = __int_as_float(0x7fc00000);
                 }
+                if (ACC && bulk) {
+                    ok = tc_mbar_wait(y_full + 8 * k, (y_parity >> k) & 1u, kI8SpinLimit) && ok;
+                    y_parity ^= 1u << k;
+                }
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    Y& o = smem_at<Y>(out + (uint32_t)((j * kI8Rows + row) * (int)sizeof(Y)));
+                    o = from_f32<Y>(ACC ? to_f32(o) + f[j] : f[j]);
+                }
+                if (bulk) fence_async_smem();
+                int8_out_sync(group);
                 if (bulk) {
-                    if (ACC) {
-                        ok = tc_mbar_wait(y_full0 + 8 * buf, (y_parity >> buf) & 1u, kI8SpinLimit) && ok;
-                        y_parity ^= 1u << buf;
+                    if (e == 0) {
+                        if (t0 + c < p.T && m0 < p.M)
+                            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                                         ::"l"(&map_y), "r"(m0), "r"((int)(t0 + c)), "r"(sb + out) : "memory");
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        Y& o = smem_at<Y>(out + (uint32_t)((j * kI8Rows + row) * sizeof(Y)));
-                        o = from_f32<Y>(ACC ? to_f32(o) + f[j] : f[j]);
-                    }
-                    fence_async_smem();
-                    int8_out_sync();
-                    if (e == 0 && t0 + c < p.T && m0 < p.M) {
-                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
-                                     ::"l"(&map_y), "r"(m0), "r"((int)(t0 + c)), "r"(sb + out) : "memory");
-                    }
-                    if (e == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                } else if (m < p.M) {
-                    Y* y = static_cast<Y*>(p.y) + (t0 + c) * p.ldy + m;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (t0 + c + j < p.T) *y = from_f32<Y>(ACC ? to_f32(*y) + f[j] : f[j]);
-                        y += p.ldy;
-                    }
+                } else {
+                    int8_copy_rows<Y, C, true>(p, out, t0 + c, m0, e);
                 }
             }
+            // this warp has read its part of the accumulators
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) int8_remote_arrive(dsmem_addr(acc_empty0 + 8 * b, 0));
         }
         if (a.bulk && e == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok && lane == 0) atomicOr(a.err, 1u);
