@@ -428,7 +428,7 @@ int run_int8(const Int8Args& p, void* stream) {
     if ((st = encode_rows(&mw, p.w, p.M, p.N, p.ldw, kI8Rows)) != FLUXBIN_OK) return st;
     if ((st = encode_rows(&mx, p.x, p.T, p.N, p.ldx, a.bn)) != FLUXBIN_OK) return st;
     CUtensorMap my = mx;
-    if (splits == 1 && !acc && (st = encode_y(&my, p, kI8OutBox, &a.bulk)) != FLUXBIN_OK) return st;
+    if (splits == 1 && (st = encode_y(&my, p, kI8OutBox, &a.bulk)) != FLUXBIN_OK) return st;
     return launch(pick_int8_tc(p.flags), dim3((unsigned)(tiles * splits)), dim3(kI8Threads),
                   (size_t)(kI8RingOff + a.stages * stage), splits, stream, mw, mx, my, a);
 }

@@ -160,6 +160,94 @@ __device__ __forceinline__ void int8_store4(const Int8Args& p, int64_t t, int m,
     }
 }
 
+// `rows` tokens of a tile of y, [rows][128 channels] of Y at byte offset `buf`
+// of the shared memory, out to y (tokens from t0, channels from m0 on) or in
+// from it, by THREADS threads (e: this one's number): 16 bytes a lane, the
+// pieces of rows that start off a 16-byte boundary shifted into place, the ends
+// of a row element by element; U rows of a thread at a time, every load before
+// the first store.
+template <typename Y, int THREADS, int U>
+__device__ __forceinline__ void int8_rows_out(const Int8Args& p, uint32_t buf, int64_t t0, int rows, int m0, int e) {
+    constexpr int kLanes = kI8Rows * (int)sizeof(Y) / 16, kPer = 16 / (int)sizeof(Y), kStep = THREADS / kLanes;
+    const int l = e % kLanes, nv = p.M - m0 < kI8Rows ? p.M - m0 : kI8Rows;
+    if (t0 + rows > p.T) rows = (int)(p.T - t0);
+    for (int j0 = e / kLanes; j0 < rows; j0 += U * kStep) {
+        uint4 piece[U];
+        Y end[U];
+        int end_at[U], piece_at[U];                                  // elements of the row, -1: none
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * kStep;
+            const Y* y = static_cast<const Y*>(p.y) + (t0 + j) * p.ldy + m0;
+            const uint32_t row = buf + (uint32_t)(j * kI8Rows * (int)sizeof(Y));
+            const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(y) & 15u;
+            const int head = off ? (int)((16u - off) / sizeof(Y)) : 0;   // elements before the first boundary
+            const int whole = nv > head ? (nv - head) / kPer : 0;        // pieces
+            piece_at[u] = j < rows && l < whole ? head + l * kPer : -1;
+            if (piece_at[u] >= 0) {
+                uint32_t w[8];
+                put(w, smem_at<const uint4>(row + 16u * l));
+                put(w + 4, off ? smem_at<const uint4>(row + 16u * l + 16u) : make_uint4(0, 0, 0, 0));
+                piece[u] = shifted<0>(w, off ? 16u - off : 0u);
+            }
+            const int el = l < head ? l : whole * kPer + l;              // what no piece covers: below 16 elements
+            end_at[u] = j < rows && el < nv ? el : -1;
+            if (end_at[u] >= 0) end[u] = smem_at<const Y>(row + (uint32_t)(el * (int)sizeof(Y)));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Y* y = static_cast<Y*>(p.y) + (t0 + j0 + u * kStep) * p.ldy + m0;
+            if (piece_at[u] >= 0) *reinterpret_cast<uint4*>(y + piece_at[u]) = piece[u];
+            if (end_at[u] >= 0) y[end_at[u]] = end[u];
+        }
+    }
+}
+template <typename Y, int THREADS, int U>
+__device__ __forceinline__ void int8_rows_in(const Int8Args& p, uint32_t buf, int64_t t0, int rows, int m0, int e) {
+    constexpr int kLanes = kI8Rows * (int)sizeof(Y) / 16, kPer = 16 / (int)sizeof(Y), kStep = THREADS / kLanes;
+    const int l = e % kLanes, nv = p.M - m0 < kI8Rows ? p.M - m0 : kI8Rows;
+    if (t0 + rows > p.T) rows = (int)(p.T - t0);
+    for (int j0 = e / kLanes; j0 < rows; j0 += U * kStep) {
+        uint4 lo[U], hi[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * kStep;
+            const Y* y = static_cast<const Y*>(p.y) + (t0 + j) * p.ldy + m0 + l * kPer;
+            const uintptr_t at = reinterpret_cast<uintptr_t>(y);
+            const uint32_t off = (uint32_t)at & 15u;
+            const int before = (int)(off / sizeof(Y)), after = off ? (int)((16u - off) / sizeof(Y)) : 0;
+            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+            if (j < rows) {
+                if (m0 + l * kPer >= before && m0 + (l + 1) * kPer + after <= p.M) {
+                    lo[u] = *reinterpret_cast<const uint4*>(at - off);
+                    if (off) hi[u] = *reinterpret_cast<const uint4*>(at - off + 16);
+                } else {
+                    // the ends of the row; put where the shift below takes them from
+                    Y el[2 * kPer];
+#pragma unroll
+                    for (int k = 0; k < 2 * kPer; ++k) {
+                        const int c = k - before;
+                        el[k] = c >= 0 && c < kPer && l * kPer + c < nv ? y[c] : from_f32<Y>(0.f);
+                    }
+                    lo[u] = *reinterpret_cast<const uint4*>(el);
+                    hi[u] = *reinterpret_cast<const uint4*>(el + kPer);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * kStep;
+            const Y* y = static_cast<const Y*>(p.y) + (t0 + j) * p.ldy + m0 + l * kPer;
+            uint32_t w[8];
+            put(w, lo[u]);
+            put(w + 4, hi[u]);
+            if (j < rows)
+                smem_at<uint4>(buf + (uint32_t)(j * kI8Rows * (int)sizeof(Y)) + 16u * l) =
+                    shifted<0>(w, (uint32_t)reinterpret_cast<uintptr_t>(y) & 15u);
+        }
+    }
+}
+
 __device__ __forceinline__ int4 add4(const int4& a, const int4& b) {
     return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
@@ -328,7 +416,7 @@ __global__ void __launch_bounds__(kI8Threads)
     const bool ok = drained && smem_at<const volatile uint32_t>(kFailed) == 0u;
 
     const uint32_t acc0 = tmem + ((uint32_t)(quarter * 32) << 16);
-    const bool bulk = !ACC && a.splits == 1 && a.bulk > (m0 + kI8Rows <= p.M ? 0 : 1);
+    const bool bulk = a.splits == 1 && a.bulk > (m0 + kI8Rows <= p.M ? 0 : 1);
     // Every stage has been consumed: the ring holds the partial sums
     // ([bn][128] integers), or the tile of y on its way out ([bn][128] of Y).
     // Groups of 16 tokens, alternately to the two warps that reach a quarter.
@@ -355,21 +443,17 @@ __global__ void __launch_bounds__(kI8Threads)
 #pragma unroll
             for (int j = 0; j < 16; ++j) f[j] = __int_as_float(0x7fc00000);
         }
-        if (bulk) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                smem_at<Y>((uint32_t)(kI8RingOff + ((c + j) * kI8Rows + row) * (int)sizeof(Y))) = from_f32<Y>(f[j]);
-        } else if (m < p.M) {
-            Y* y = static_cast<Y*>(p.y) + (t0 + c) * p.ldy + m;
+        if (ACC && m < p.M) {
+            const Y* y = static_cast<const Y*>(p.y) + (t0 + c) * p.ldy + m;
             float old[16];
-            if (ACC) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) old[j] = c + j < nt ? to_f32(y[j * p.ldy]) : 0.f;
-            }
+            for (int j = 0; j < 16; ++j) old[j] = c + j < nt ? to_f32(y[j * p.ldy]) : 0.f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (c + j < nt) y[j * p.ldy] = from_f32<Y>(ACC ? f[j] + old[j] : f[j]);
+            for (int j = 0; j < 16; ++j) f[j] += old[j];
         }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            smem_at<Y>((uint32_t)(kI8RingOff + ((c + j) * kI8Rows + row) * (int)sizeof(Y))) = from_f32<Y>(f[j]);
     }
     if (bulk) fence_async_smem();
     tc_fence_before();
@@ -387,6 +471,7 @@ __global__ void __launch_bounds__(kI8Threads)
             asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
         }
     }
+    if (a.splits == 1 && !bulk) int8_rows_out<Y, kI8Threads, 4>(p, kI8RingOff, t0, nt, m0, tid);
     if (a.splits > 1) {
         int8_cluster_sync();
         // one lane asks each CTA whether it failed, while the sums are on their way

@@ -101,38 +101,6 @@ __device__ __forceinline__ void int8_ld(uint32_t taddr, int (&v)[C]) {
     else int8_ld16(taddr, v);
 }
 
-// Rows of y (tokens t0 .., channels m0 ..) to or from a staging buffer, by the
-// 128 threads of a group: a warp per row, four channels a lane where the rows
-// allow it.
-template <typename Y, int C, bool OUT>
-__device__ __forceinline__ void int8_copy_rows(const Int8Args& p, uint32_t buf, int64_t t0, int m0, int e) {
-    const int lane = e & 31;
-    struct alignas(4 * sizeof(Y)) Quad { Y v[4]; };
-#pragma unroll
-    for (int i = 0; i < C / 4; ++i) {
-        const int j = (e >> 5) + 4 * i;
-        if (t0 + j >= p.T) continue;
-        Y* y = static_cast<Y*>(p.y) + (t0 + j) * p.ldy + m0;
-        const uint32_t row = buf + (uint32_t)(j * kI8Rows * (int)sizeof(Y));
-        if (p.vec4 && m0 + 4 * lane + 4 <= p.M) {
-            Quad& o = smem_at<Quad>(row + (uint32_t)(4 * lane * (int)sizeof(Y)));
-            if (OUT) *reinterpret_cast<Quad*>(y + 4 * lane) = o;
-            else o = *reinterpret_cast<const Quad*>(y + 4 * lane);
-        } else {
-            // (with four channels a lane only the row's ragged end)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int ch = p.vec4 ? 4 * lane + k : lane + 32 * k;
-                if (m0 + ch < p.M) {
-                    Y& o = smem_at<Y>(row + (uint32_t)(ch * (int)sizeof(Y)));
-                    if (OUT) y[ch] = o;
-                    else o = y[ch];
-                }
-            }
-        }
-    }
-}
-
 struct Int8PairTile {
     int tm, tt;
 };
@@ -329,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 }
                 if (!ACC || !bulk) int8_out_sync(group);
                 if (ACC && !bulk) {
-                    int8_copy_rows<Y, C, false>(p, out, t0 + c, m0, e);
+                    int8_rows_in<Y, 128, 2>(p, out, t0 + c, C, m0, e);
                     int8_out_sync(group);
                 }
                 float f[C];
@@ -366,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 } else {
-                    int8_copy_rows<Y, C, true>(p, out, t0 + c, m0, e);
+                    int8_rows_out<Y, 128, 2>(p, out, t0 + c, C, m0, e);
                 }
             }
             // this warp has read its part of the accumulators

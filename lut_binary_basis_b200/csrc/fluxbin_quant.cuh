@@ -100,27 +100,6 @@ struct Raw {
     uint32_t w[kWords];
 };
 
-// The 16 bytes that start `by` bytes (below 16, a multiple of 2) into w[K..K+7].
-template <int K>
-__device__ __forceinline__ uint4 shifted(const uint32_t* w, uint32_t by) {
-    uint32_t x[6], y[5], r[4];
-#pragma unroll
-    for (int k = 0; k < 6; ++k) x[k] = (by & 8u) ? w[K + k + 2] : w[K + k];
-#pragma unroll
-    for (int k = 0; k < 5; ++k) y[k] = (by & 4u) ? x[k + 1] : x[k];
-    const uint32_t sel = (by & 2u) ? 0x5432u : 0x3210u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = __byte_perm(y[k], y[k + 1], sel);
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
-__device__ __forceinline__ void put(uint32_t* w, const uint4& v) {
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-}
-
 // Elements n .. n+7 of a row of N (zeros past its end).  VEC: the row's
 // length is a multiple of 8 and it starts at a 16-byte boundary.
 template <bool VEC, typename T>
