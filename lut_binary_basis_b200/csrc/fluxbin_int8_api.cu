@@ -309,7 +309,7 @@ int resident_clusters(const Int8Device& d, int splits) {
 // (128x11008x4096, 86 tiles: 3 splits on two CTAs per SM 14.6, none on one
 // 16.2).  One CTA per SM is enough where a CTA's share is down to 8 stages
 // (16x4096x4096 with 4 splits 7.4, with 8 7.6; 16x4096x11008 12.8 and 11.7).
-int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
+int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out, double* us) {
     Int8TcArgs& a = *out;
     a.kblocks = (p.N + kI8K - 1) / kI8K;
     // token tiles of equal size, a multiple of 16
@@ -318,7 +318,7 @@ int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
     const int64_t tiles = (int64_t)a.tiles_t * (((int64_t)p.M + kI8Rows - 1) / kI8Rows);
     const int one = (int)std::min<int64_t>(kI8MaxSplits, d.sm_count / tiles);
     const int two = (int)std::min<int64_t>(kI8MaxSplits, 2 * d.sm_count / tiles);
-    const bool whole = a.bn > 192 || (a.bn > 112 && one * tiles * 4 >= 3 * d.sm_count);
+    const bool whole = a.bn > 160 || (a.bn > 112 && one * tiles * 4 >= 3 * d.sm_count);
     int splits = whole || (one >= 1 && a.kblocks <= 8 * one) ? one : two;
     splits = std::max(1, std::min(splits, a.kblocks / 2));
     const int stage = int8_stage_bytes(a.bn);
@@ -333,6 +333,13 @@ int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
         // all fit, 15.0)
         if (splits == 1 || resident_clusters(d, splits) * (whole ? 1 : 2) >= tiles) break;
     }
+    // The call's time, to be set against the pair kernel's: a fixed part (the
+    // outputs, the clusters' meeting) and the stages of a CTA in each wave.
+    const int64_t slots = (whole ? 1 : 2) * (int64_t)d.sm_count;
+    const int64_t waves = (tiles * splits + slots - 1) / slots;
+    const double fixed = splits == 1 ? 4.0 + 0.01 * a.bn : 3.8 + 0.03 * std::min(a.bn, 128) + 0.012 * std::max(a.bn - 128, 0);
+    const double stage_us = whole ? std::max(0.25, 0.00125 * a.bn) : tiles * splits > d.sm_count ? 0.42 : 0.25;
+    *us = fixed + (double)waves * ((a.kblocks + splits - 1) / splits) * stage_us;
     return tiles;
 }
 
@@ -342,33 +349,27 @@ int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out) {
 // 192 / 256 tokens a tile: 13.6 / 14.6 / 16.0 us).  512x4096x4096: 128 tokens,
 // 64 tiles in one round, 14.7 us; 256 tokens 16.2.  512x11008x4096, two rounds
 // either way: 192 tokens 25.1, 256 tokens 26.0.
-int pair_tile(const Int8Args& p, const Int8Device& d) {
+int pair_tile(const Int8Args& p, const Int8Device& d, double* us) {
     const int64_t tiles_m = ((int64_t)p.M + 2 * kI8Rows - 1) / (2 * kI8Rows), pairs = d.sm_count / 2;
     int best = kI8MaxBn;
-    int64_t cost = INT64_MAX;
+    int64_t cost = INT64_MAX, rounds = 1;
     for (int bn = kI8MaxBn; bn >= 96; bn -= 32) {
         const int64_t r = (tiles_m * (((int64_t)p.T + bn - 1) / bn) + pairs - 1) / pairs;
         if (r * (384 + bn / 2) < cost) {
             cost = r * (384 + bn / 2);
             best = bn;
+            rounds = r;
         }
     }
+    *us = 4.0 + (double)rounds * ((p.N + kI8K - 1) / kI8K) * 0.24;
     return best;
 }
 
-// Pairs from 257 tokens on, where their tiles fill half of the GPU
-// (333x4096x11008: 64 tiles of the split kernel 24.1 us, 64 of pairs 28.0;
-// 512x4096x4096 16.0 and 14.7; 256x11008x4096 17.4 and 18.2).
-bool use_pairs(const Int8Args& p, const Int8Device& d) {
-    const int64_t tiles = ((int64_t)p.M + 255) / 256 * (((int64_t)p.T + 127) / 128);
-    return p.T > kI8MaxBn && tiles * 4 >= 3 * (d.sm_count / 2);
-}
-
-int run_pairs(const Int8Args& p, const Int8Device& d, void* stream) {
+int run_pairs(const Int8Args& p, const Int8Device& d, int bn, void* stream) {
     Int8PairArgs a = {};
     a.p = p;
     a.kblocks = (p.N + kI8K - 1) / kI8K;
-    a.bn = pair_tile(p, d);
+    a.bn = bn;
     a.tiles_t = (int)(((int64_t)p.T + a.bn - 1) / a.bn);
     a.tiles_m = (int)(((int64_t)p.M + 2 * kI8Rows - 1) / (2 * kI8Rows));
     a.tiles = (int64_t)a.tiles_t * a.tiles_m;
@@ -413,10 +414,17 @@ int run_int8(const Int8Args& p, void* stream) {
     Int8Device d;
     int st = int8_device(&d);
     if (st != FLUXBIN_OK) return st;
-    if (use_pairs(p, d)) return run_pairs(p, d, stream);
+    // The kernel whose estimated time is shorter.  Both sides measured (B200,
+    // us a call, single / pairs): 128x4096x4096 10.6 / 12.5, 192 tokens 11.6 /
+    // 12.5, 512 tokens 13.3 / 11.9; 256x8192x8192 20.6 / 20.8, 512 tokens 31.1 /
+    // 29.9; 512x4096x11008 22.6 / 22.8, 640 tokens 29.2 / 24.6; 160x28672x8192
+    // 46.5 / 48.6, 176 tokens 67.7 / 50.5; 128x2048x2048 8.6 / 8.0.
+    double us_single = 0., us_pairs = 0.;
     Int8TcArgs a = {};
     a.p = p;
-    const int64_t tiles = plan_int8(p, d, &a);
+    const int64_t tiles = plan_int8(p, d, &a, &us_single);
+    const int pair_bn = pair_tile(p, d, &us_pairs);
+    if (us_pairs < us_single) return run_pairs(p, d, pair_bn, stream);
     const int stage = int8_stage_bytes(a.bn), splits = a.splits;
     a.tmem_cols = 32;
     while ((int)a.tmem_cols < a.bn) a.tmem_cols *= 2;

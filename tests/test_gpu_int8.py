@@ -226,7 +226,7 @@ def test_many_tokens():
     assert bool((buf[:, 999] == 0).all()) and bool((buf[:, 1000 + M] == 0).all())
 
 
-@pytest.mark.parametrize("T,M,N", [(20, 300, 4096), (200, 2000, 1000), (600, 4096, 512)])
+@pytest.mark.parametrize("T,M,N", [(20, 300, 4096), (200, 2000, 1000), (600, 4096, 512), (700, 9000, 300), (64, 20000, 256)])
 def test_waits_that_give_up(T, M, N):
     """The bounded waits' give-up path: NaN outputs, the status bit (read and
     cleared), and a correct next call."""
