@@ -187,9 +187,9 @@ const char* fluxbin_status_string(int status);
 const char* fluxbin_last_error(void);
 
 /*
- * Device-side status of the current device.  Bit 0: a tensor-core launch gave
- * up one of its bounded waits (never expected outside the test hook above;
- * the outputs it owned are then NaN).  Bit 1: a tensor-core launch could not
+ * Device-side status of the current device.  Bit 0: a tensor-core launch
+ * (fluxbin_int8_linear among them) gave up one of its bounded waits (never
+ * expected outside the test hooks; the outputs it owned are then NaN).  Bit 1: a tensor-core launch could not
  * confirm that its matrix operations had finished and kept its tensor memory
  * instead of releasing it under them (never expected).  The LUT path has no
  * waits that can give up: its only cross-CTA wait is the hardware cluster
@@ -462,7 +462,7 @@ int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, co
  * The 8-bit integer product with a scale for each channel and each token:
  *   y[t][m] (+)= xscale[t] * wscale[m] * sum_n x[t][n] * w[m][n]
  * The sum is exact (any int8 codes, -128 among them); it is rounded to fp32
- * once, multiplied by the scales in fp32 and rounded to y's type (with
+ * once, multiplied by the product of the two scales in fp32 and rounded to y's type (with
  * FLUXBIN_FLAG_ACCUMULATE after the addition to y).  The result does not
  * depend on T: a token's row is the same bit for bit alone and in a batch.
  *   M, N     output features (channels) and input features
@@ -474,7 +474,8 @@ int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, co
  *            stream has finished), FLUXBIN_FLAG_TEST_WAIT_TIMEOUT (test hook: the kernel's
  *            copies are never issued and its waits give up after a few polls: the outputs
  *            become NaN and bit 0 of fluxbin_device_status is set)
- * M == 0 returns FLUXBIN_OK without launching; N == 0 is a product of zero.
+ * M and T are at most 2^31 - 1024 (UNSUPPORTED above).  M == 0 returns FLUXBIN_OK
+ * without launching; N == 0 is a product of zero.
  * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
  */
 int fluxbin_int8_linear(int32_t M, int32_t N, const int8_t* d_w, int64_t ldw, const float* d_wscale,

@@ -20,6 +20,7 @@ namespace fluxbin {
 namespace {
 
 constexpr int32_t kInt8MaxN = 131071;   // 128 * 128 * N < 2^31
+constexpr int32_t kInt8MaxRows = INT32_MAX - 1023;   // a tile's last row still has a 32-bit number
 
 constexpr int64_t kMaxPitch = (int64_t)1 << 39;   // beyond any device memory: offsets stay far from 2^63
 
@@ -490,7 +491,7 @@ int fluxbin_int8_linear(int32_t M, int32_t N, const int8_t* d_w, int64_t ldw, co
     if ((flags & FLUXBIN_FLAG_Y_FP32) && (flags & FLUXBIN_FLAG_BF16)) return FLUXBIN_ERR_INVALID_ARG;
     if (M < 0 || N < 0 || T < 0 || bad_pitch(ldw, N) || bad_pitch(ldx, N) || bad_pitch(ldy, M))
         return FLUXBIN_ERR_BAD_SHAPE;
-    if (N > kInt8MaxN) return FLUXBIN_ERR_UNSUPPORTED;
+    if (N > kInt8MaxN || M > kInt8MaxRows || T > kInt8MaxRows) return FLUXBIN_ERR_UNSUPPORTED;
     if (M == 0 || T == 0) return FLUXBIN_OK;
     if (!d_y || !d_wscale || !d_xscale || (N > 0 && (!d_w || !d_x))) return FLUXBIN_ERR_INVALID_ARG;
     const int ys = (flags & FLUXBIN_FLAG_Y_FP32) ? 4 : 2;

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kI8Threads)
     const bool ok = drained && smem_at<const volatile uint32_t>(kFailed) == 0u;
 
     const uint32_t acc0 = tmem + ((uint32_t)(quarter * 32) << 16);
-    const bool bulk = a.splits == 1 && a.bulk > (m0 + kI8Rows <= p.M ? 0 : 1);
+    const bool bulk = a.splits == 1 && a.bulk > (p.M - m0 >= kI8Rows ? 0 : 1);
     // Every stage has been consumed: the ring holds the partial sums
     // ([bn][128] integers), or the tile of y on its way out ([bn][128] of Y).
     // Groups of 16 tokens, alternately to the two warps that reach a quarter.

@@ -249,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             const int64_t t0 = (int64_t)t.tt * a.bn;
             // TMA writes whole 16-byte pieces: a ragged last tile only where
             // M ends on one
-            const bool bulk = a.bulk > (m0 + kI8Rows <= p.M ? 0 : 1);
+            const bool bulk = a.bulk > (p.M - m0 >= kI8Rows ? 0 : 1);
             // requests a chunk's y (accumulation) into its staging buffer
             const auto load_y = [&](int q) {
                 const int k = (q >> 1) & 1;

@@ -63,6 +63,8 @@ _lib = None
 
 def lib():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -397,29 +399,34 @@ def _vector(t, name: str, n: int, dtypes, device) -> None:
         raise ValueError(f"{name} is not contiguous")
 
 
-def _on_device(device, call, *args, stream=None) -> None:
-    """Runs a device call with the tensors' own device current, on ``stream``
-    or that device's current stream."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}, not on a CUDA device")
-    if device.index == torch.cuda.current_device():
-        call(*args, stream)
-        return
-    with torch.cuda.device(device):
-        call(*args, stream)
-
-
+_torch = None          # torch, once a method below has needed it
 _float_types = None
 
 
 def _floats():
     """(fp16, bf16, fp32) as torch types."""
-    global _float_types
+    global _torch, _float_types
     if _float_types is None:
         import torch
-        _float_types = (torch.float16, torch.bfloat16, torch.float32)
+        _torch, _float_types = torch, (torch.float16, torch.bfloat16, torch.float32)
     return _float_types
+
+
+def _call(name: str, device, stream, *args) -> None:
+    """Makes a device call with the tensors' own device current, on ``stream``
+    or that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a CUDA device")
+    index = device.index
+    s = _torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    fn = getattr(lib(), name)
+    if index == _torch.cuda.current_device():
+        st = fn(*args, s)
+    else:
+        with _torch.cuda.device(device):
+            st = fn(*args, s)
+    if st != 0:
+        raise FluxbinError(st, name)
 
 
 class QuantRows:
@@ -448,22 +455,24 @@ class QuantRows:
 
     def rows(self, T: int) -> "QuantRows":
         """The first T rows (sharing memory)."""
+        if not 0 <= T <= self.T:
+            raise ValueError(f"{T} of {self.T} rows")
         return QuantRows(self.q[:T], self.scale[:T])
 
     def quantize(self, x, stream=None) -> None:
         """Codes and scales of the rows of x (fp16 or bf16 [T][N])."""
         e = _floats()[:2]
         ldx = _matrix(x, "x", (self.T, self.N), e, self.device)
-        _on_device(self.device, fluxbin_quant_rows, self.T, self.N, x, ldx, self.q, self.ldq, self.scale,
-                   FLAG_BF16 if x.dtype == e[1] else 0, stream=stream)
+        _call("fluxbin_quant_rows", self.device, stream, self.T, self.N, x.data_ptr(), ldx, self.q.data_ptr(), self.ldq,
+              self.scale.data_ptr(), FLAG_BF16 if x.dtype == e[1] else 0)
 
     def silu_mul(self, gate, up, stream=None) -> None:
         """Codes and scales of silu(gate) * up (both fp16 or both bf16 [T][N])."""
         e = _floats()[:2]
         ldg = _matrix(gate, "gate", (self.T, self.N), e, self.device)
         ldu = _matrix(up, "up", (self.T, self.N), (gate.dtype,), self.device)
-        _on_device(self.device, fluxbin_silu_mul_quant, self.T, self.N, gate, ldg, up, ldu, self.q, self.ldq,
-                   self.scale, FLAG_BF16 if gate.dtype == e[1] else 0, stream=stream)
+        _call("fluxbin_silu_mul_quant", self.device, stream, self.T, self.N, gate.data_ptr(), ldg, up.data_ptr(), ldu,
+              self.q.data_ptr(), self.ldq, self.scale.data_ptr(), FLAG_BF16 if gate.dtype == e[1] else 0)
 
     def rmsnorm(self, h, gamma, eps: float, delta=None, h_out=None, stream=None) -> None:
         """Codes and scales of rmsnorm(h + delta) * gamma; ``h_out`` (may be h)
@@ -475,8 +484,8 @@ class QuantRows:
         ldd = 0 if delta is None else _matrix(delta, "delta", (self.T, self.N), (gamma.dtype,), self.device)
         ldo = 0 if h_out is None else _matrix(h_out, "h_out", (self.T, self.N), (h.dtype,), self.device)
         flags = (FLAG_BF16 if gamma.dtype == bf16 else 0) | (FLAG_H_FP32 if h.dtype == f32 else 0)
-        _on_device(self.device, fluxbin_rmsnorm_quant, self.T, self.N, h, ldh, delta, ldd, gamma, eps, h_out, ldo,
-                   self.q, self.ldq, self.scale, flags, stream=stream)
+        _call("fluxbin_rmsnorm_quant", self.device, stream, self.T, self.N, h.data_ptr(), ldh, _dptr(delta), ldd,
+              gamma.data_ptr(), float(eps), _dptr(h_out), ldo, self.q.data_ptr(), self.ldq, self.scale.data_ptr(), flags)
 
 
 class Int8Layer:
@@ -518,5 +527,5 @@ class Int8Layer:
             raise ValueError(f"rows of {rows.N} codes on {rows.device} for a layer of {self.N} on {self.device}")
         ldy = _matrix(y, "y", (rows.T, self.M), e, self.device)
         flags |= FLAG_BF16 if y.dtype == bf16 else FLAG_Y_FP32 if y.dtype == f32 else 0
-        _on_device(self.device, fluxbin_int8_linear, self.M, self.N, self.w, self.ldw, self.scale, rows.q, rows.ldq,
-                   rows.scale, rows.T, y, ldy, flags, stream=stream)
+        _call("fluxbin_int8_linear", self.device, stream, self.M, self.N, self.w.data_ptr(), self.ldw,
+              self.scale.data_ptr(), rows.q.data_ptr(), rows.ldq, rows.scale.data_ptr(), rows.T, y.data_ptr(), ldy, flags)

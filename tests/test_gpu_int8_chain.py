@@ -167,3 +167,67 @@ def test_other_device_and_stream():
         rows = fluxbin.QuantRows.empty(2, 64, "cuda:1")
         rows.quantize(torch.randn(2, 64, device="cuda:1").half())
         torch.cuda.synchronize(1)
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has to be warmed up: the process's first calls are captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from lut_binary_basis_b200 import fluxbin
+torch.zeros(1, device="cuda")
+out = []
+for T, M in ((1, 64), (40, 256), (300, 20000)):
+    x = torch.ones(T, 96, device="cuda").half()
+    rows = fluxbin.QuantRows.empty(T, 96)
+    layer = fluxbin.Int8Layer(torch.ones(M, 96, dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda"))
+    y = torch.zeros(T, M, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rows.quantize(x)
+        layer.linear(rows, y)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.allclose(y, torch.full_like(y, 96.0), rtol=1e-6), (T, M)
+assert fluxbin.fluxbin_device_status() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_host_threads():
+    """Calls from two host threads at once, each on its own stream."""
+    import threading
+    results = {}
+
+    def work(k):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            g = torch.Generator("cuda").manual_seed(k)
+            ok = True
+            for T, M, N in ((1, 512, 512), (33, 700, 900), (300, 5000, 400)) * 5:
+                x = torch.randn(T, N, generator=g, device="cuda").half()
+                w = torch.randint(-127, 128, (M, N), generator=g, device="cuda", dtype=torch.int8)
+                wp = torch.zeros(M, -(-N // 16) * 16, dtype=torch.int8, device="cuda")[:, :N]
+                wp.copy_(w)
+                layer = fluxbin.Int8Layer(wp, torch.ones(M, device="cuda"))
+                rows = fluxbin.QuantRows.empty(T, N)
+                rows.quantize(x)
+                y = torch.empty(T, M, device="cuda")
+                layer.linear(rows, y)
+                want = (rows.q.double() @ w.double().t()) * rows.scale.double()[:, None]
+                ok = ok and bool(((y.double() - want).abs() <= want.abs() * 2.0 ** -22).all())
+            s.synchronize()
+            results[k] = ok
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in (1, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    assert results == {1: True, 2: True}

@@ -70,6 +70,7 @@ def test_rmsnorm_quant_refusals(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(T=0), 0), (dict(M=0), 0), (dict(T=0, x=0, xs=0, y=0), 0),
     (dict(T=-1), SHAPE), (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(ldw=16), SHAPE), (dict(ldx=16), SHAPE), (dict(ldy=31), SHAPE),
+    (dict(M=(1 << 31) - 1, ldy=(1 << 31) - 1), UNSUPPORTED), (dict(T=(1 << 31) - 1), UNSUPPORTED),
     (dict(ldy=1 << 41), SHAPE), (dict(N=BIG + 1, ldw=BIG + 1, ldx=BIG + 1), UNSUPPORTED),
     (dict(w=0), INVALID), (dict(ws=0), INVALID), (dict(x=0), INVALID), (dict(xs=0), INVALID), (dict(y=0), INVALID),
     (dict(flags=fluxbin.FLAG_Y_FP32 | fluxbin.FLAG_BF16), INVALID), (dict(flags=fluxbin.FLAG_PATH_TC), INVALID),
@@ -120,6 +121,9 @@ def test_binding_checks_shapes_types_and_devices():
             layer.linear(rows, bad)
     e = fluxbin.QuantRows.empty(3, 21, "cpu")
     assert e.q.shape == (3, 21) and e.ldq == 32 and e.rows(2).T == 2
+    for t in (4, -1):
+        with pytest.raises(ValueError):
+            e.rows(t)
 
 
 def test_layer_from_host():
