@@ -58,10 +58,24 @@ __global__ void __launch_bounds__(32 * kMvWarps) fluxbin_int8_mv_kernel(const In
     const int m0 = blockIdx.x * kMvRows;
     asm volatile("griddepcontrol.launch_dependents;");
     const bool early = (p.flags & kInt8Early) != 0;
-    if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
     // rows past the last one repeat it; their sums are not written
     const int8_t* w0 = p.w + (int64_t)min(m0 + g, p.M - 1) * p.ldw;
     const int8_t* w1 = p.w + (int64_t)min(m0 + g + 8, p.M - 1) * p.ldw;
+    if (!early) {
+        // into L2 only: that may run ahead of the preceding kernel even if
+        // that one writes the weights
+        if (q == 0) {
+#pragma unroll
+            for (int i = 0; i < kMvBatch; ++i) {
+                const int n = (warp + i * kMvWarps) * kMvSegment;
+                if (n < p.N) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + n));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + n));
+                }
+            }
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
     const int segments = (p.N + kMvSegment - 1) / kMvSegment;
 
     int c[NT][4] = {};

@@ -94,6 +94,12 @@ __device__ __forceinline__ void int8_tma(uint32_t dst, const CUtensorMap* map, i
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
+// The same box into L2 only.  L2 is where all writes meet: a prefetch may run
+// ahead of the preceding kernel even if that one writes the weights.
+__device__ __forceinline__ void int8_prefetch(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
 __device__ __forceinline__ void int8_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -248,6 +254,15 @@ __device__ __forceinline__ void int8_rows_in(const Int8Args& p, uint32_t buf, in
     }
 }
 
+// The 128 channels from m0 on of a token of y into L2, ahead of an accumulation.
+template <typename Y>
+__device__ __forceinline__ void int8_prefetch_row(const Int8Args& p, int64_t t, int m0) {
+    const int n = (p.M - m0 < kI8Rows ? p.M - m0 : kI8Rows) * (int)sizeof(Y);
+    const char* row = reinterpret_cast<const char*>(static_cast<const Y*>(p.y) + t * p.ldy + m0);
+    for (int o = 0; o < n; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + o));
+    if (n > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + n - 1));
+}
+
 __device__ __forceinline__ int4 add4(const int4& a, const int4& b) {
     return make_int4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
@@ -330,11 +345,14 @@ __global__ void __launch_bounds__(kI8Threads)
             const bool early = (p.flags & kInt8Early) != 0;
             const int ahead = nk < a.stages ? nk : a.stages;
             const int nload = a.test_stall ? 0 : nk;
-            if (early && nload) {
-                // the ring's first weights before the preceding kernel has finished
-                for (int s = 0; s < ahead; ++s) {
+            // the ring's first weights before the preceding kernel has
+            // finished, at least into L2
+            for (int s = 0; s < ahead && nload; ++s) {
+                if (early) {
                     int8_expect(full0 + 8 * s, stage_bytes);
                     int8_tma(ring + s * stage_bytes, &map_w, (kb0 + s) * kI8K, m0, full0 + 8 * s);
+                } else {
+                    int8_prefetch(&map_w, (kb0 + s) * kI8K, m0);
                 }
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -394,6 +412,7 @@ __global__ void __launch_bounds__(kI8Threads)
     const int64_t t0 = (int64_t)tile_t * a.bn;
     const int nt = (int)(p.T - t0 < a.bn ? p.T - t0 : a.bn);
     if (tid < a.bn) smem_at<float>(kI8SxOff + 4 * tid) = tid < nt ? __ldg(p.sx + t0 + tid) : 0.f;
+    if (ACC && a.splits == 1 && tid < nt) int8_prefetch_row<Y>(p, t0 + tid, m0);
     const int quarter = warp & 3;                // the lanes of tensor memory that this warp reaches
     const int row = quarter * 32 + lane, m = m0 + row;
     const int mq = 4 * lane;                     // the four channels of the split's sums
@@ -417,6 +436,10 @@ __global__ void __launch_bounds__(kI8Threads)
 
     const uint32_t acc0 = tmem + ((uint32_t)(quarter * 32) << 16);
     const bool bulk = a.splits == 1 && a.bulk > (p.M - m0 >= kI8Rows ? 0 : 1);
+    if (ACC && a.splits == 1) {
+        int8_rows_in<Y, kI8Threads, 4>(p, kI8RingOff, t0, nt, m0, tid);
+        __syncthreads();
+    }
     // Every stage has been consumed: the ring holds the partial sums
     // ([bn][128] integers), or the tile of y on its way out ([bn][128] of Y).
     // Groups of 16 tokens, alternately to the two warps that reach a quarter.
@@ -443,17 +466,11 @@ __global__ void __launch_bounds__(kI8Threads)
 #pragma unroll
             for (int j = 0; j < 16; ++j) f[j] = __int_as_float(0x7fc00000);
         }
-        if (ACC && m < p.M) {
-            const Y* y = static_cast<const Y*>(p.y) + (t0 + c) * p.ldy + m;
-            float old[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) old[j] = c + j < nt ? to_f32(y[j * p.ldy]) : 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] += old[j];
+        for (int j = 0; j < 16; ++j) {
+            Y& o = smem_at<Y>((uint32_t)(kI8RingOff + ((c + j) * kI8Rows + row) * (int)sizeof(Y)));
+            o = from_f32<Y>(ACC ? to_f32(o) + f[j] : f[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            smem_at<Y>((uint32_t)(kI8RingOff + ((c + j) * kI8Rows + row) * (int)sizeof(Y))) = from_f32<Y>(f[j]);
     }
     if (bulk) fence_async_smem();
     tc_fence_before();

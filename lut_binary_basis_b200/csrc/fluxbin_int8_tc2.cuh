@@ -163,13 +163,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             const int half = a.bn / 2;
             const uint32_t bar0 = dsmem_addr(full0, 0);   // the leader's full barriers
             int pre = 0;                           // stages whose weights were requested early
-            if (early && !a.test_stall && first < a.tiles) {
+            if (!a.test_stall && first < a.tiles) {
+                // the ring's first weights before the preceding kernel has
+                // finished, at least into L2
                 const Int8PairTile t = int8_pair_tile(a, first);
-                pre = a.kblocks < kI8PairStages ? a.kblocks : kI8PairStages;
-                for (int s = 0; s < pre; ++s) {
-                    if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
-                    int8_pair_tma(ring + s * stage_bytes, &map_w, s * kI8K, (t.tm * 2 + rank) * kI8Rows, bar0 + 8 * s);
+                const int ahead = a.kblocks < kI8PairStages ? a.kblocks : kI8PairStages;
+                const int wy = (t.tm * 2 + rank) * kI8Rows;
+                for (int s = 0; s < ahead; ++s) {
+                    if (early) {
+                        if (rank == 0) int8_expect(full0 + 8 * s, 2 * stage_bytes);
+                        int8_pair_tma(ring + s * stage_bytes, &map_w, s * kI8K, wy, bar0 + 8 * s);
+                    } else {
+                        int8_prefetch(&map_w, s * kI8K, wy);
+                    }
                 }
+                if (early) pre = ahead;
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
             int s = 0;
@@ -262,6 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 const int c = tid - 64;
                 smem_at<float>(kI8PairSxOff + (b * kI8MaxBn + c) * 4) = c < a.bn && t0 + c < p.T ? __ldg(p.sx + t0 + c) : 0.f;
             }
+            if (ACC && !bulk && tid - 64 < a.bn && t0 + tid - 64 < p.T) int8_prefetch_row<Y>(p, t0 + tid - 64, m0);
             if (ACC) {                             // (the tile before may have gone out by plain stores)
                 fence_async_smem();
                 int8_out_sync(group);

@@ -231,3 +231,28 @@ def test_two_host_threads():
     for t in threads:
         t.join(timeout=120)
     assert results == {1: True, 2: True}
+
+
+@pytest.mark.parametrize("T,M,N", [(1, 700, 1000), (16, 300, 3000), (40, 1000, 1500), (300, 9000, 500)])
+def test_weights_written_by_the_preceding_kernel(T, M, N):
+    """Without FLAG_EARLY_WEIGHTS the weights may come from the kernel before,
+    which a programmatic dependent launch overlaps: new weights every call."""
+    g = torch.Generator("cuda").manual_seed(7)
+    wrows, xrows = fluxbin.QuantRows.empty(M, N), fluxbin.QuantRows.empty(T, N)
+    xrows.quantize(torch.randn(T, N, generator=g, device="cuda").half())
+    layer = fluxbin.Int8Layer(wrows.q, wrows.scale)
+    dense = [torch.randn(M, N, generator=g, device="cuda").half() for _ in range(4)]
+    ys = [torch.empty(T, M, device="cuda") for _ in range(12)]
+    want = []
+    for d in dense:
+        wrows.quantize(d)
+        torch.cuda.synchronize()
+        want.append((xrows.q.double() @ wrows.q.double().t()) * xrows.scale.double()[:, None] * wrows.scale.double())
+    torch.cuda.synchronize()
+    for i, y in enumerate(ys):
+        wrows.quantize(dense[i % 4])
+        layer.linear(xrows, y)
+    torch.cuda.synchronize()
+    for i, y in enumerate(ys):
+        # three roundings of 2^-24 each, as in the single-operator tests
+        assert bool(((y.double() - want[i % 4]).abs() <= 3.01 * ref.EPS24 * want[i % 4].abs()).all()), i
