@@ -412,7 +412,7 @@ int fluxbin_linear_static_scratch(const fluxbin_layer_desc* desc,
  * captured graphs may run at the same time.  Launches are programmatic
  * dependent launches; every array is read and written only after the
  * preceding kernel on the stream has completed, except as
- * FLUXBIN_FLAG_EARLY_WEIGHTS says.
+ * FLUXBIN_FLAG_EARLY_WEIGHTS says (weights may be prefetched into L2 before).
  * N is at most 131071 (UNSUPPORTED above): the 32-bit sum of N products of
  * two codes cannot overflow.  T == 0 returns FLUXBIN_OK without launching.
  */

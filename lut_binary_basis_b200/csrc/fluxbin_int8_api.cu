@@ -308,13 +308,13 @@ int resident_clusters(const Int8Device& d, int splits) {
 //
 // A tile's K is split until the CTAs fill one wave of the GPU, never more
 // (B200, us a call, a graph of calls on rotated weights; splits 1 / 3 / 4:
-// 16x11008x4096, 86 tiles on 296 slots 14.3 / 11.2 / 16.3 with the fourth in a
+// 16x11008x4096, 86 tiles on 296 slots 11.0 / 9.6 / 13.6 with the fourth in a
 // second wave).  Two CTAs per SM (112 KB each) as long as that leaves a ring of
-// three stages or more; wider tiles take the whole SM (128x4096x4096 10.8
-// against 11.4), unless its 148 slots would stay a quarter empty
-// (128x11008x4096, 86 tiles: 3 splits on two CTAs per SM 14.6, none on one
-// 16.2).  One CTA per SM is enough where a CTA's share is down to 8 stages
-// (16x4096x4096 with 4 splits 7.4, with 8 7.6; 16x4096x11008 12.8 and 11.7).
+// three stages or more; from 113 tokens on a CTA takes the whole SM if half of
+// them find work (128x4096x4096 9.1 against 9.9; 128x11008x4096, 86 tiles:
+// unsplit 12.7, 3 splits on two CTAs per SM 13.4).  One CTA per SM is enough
+// where a CTA's share is down to 8 stages (32x4096x4096 with 4 splits 6.5, with
+// 8 6.7; 32x4096x11008 11.4 and 11.0).
 int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out, double* us) {
     Int8TcArgs& a = *out;
     a.kblocks = (p.N + kI8K - 1) / kI8K;
@@ -324,7 +324,7 @@ int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out, doubl
     const int64_t tiles = (int64_t)a.tiles_t * (((int64_t)p.M + kI8Rows - 1) / kI8Rows);
     const int one = (int)std::min<int64_t>(kI8MaxSplits, d.sm_count / tiles);
     const int two = (int)std::min<int64_t>(kI8MaxSplits, 2 * d.sm_count / tiles);
-    const bool whole = a.bn > 160 || (a.bn > 112 && one * tiles * 4 >= 3 * d.sm_count);
+    const bool whole = a.bn > 160 || (a.bn > 112 && one * tiles * 2 >= d.sm_count);
     int splits = whole || (one >= 1 && a.kblocks <= 8 * one) ? one : two;
     splits = std::max(1, std::min(splits, a.kblocks / 2));
     const int stage = int8_stage_bytes(a.bn);
@@ -335,8 +335,8 @@ int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out, doubl
         a.stages = std::max(2, std::min(std::min(kI8MaxStages, per_cta), room));
         // the ring holds the tile's partial sums, or its y, at the end
         a.stages = std::max(a.stages, (a.bn * kI8Rows * 4 + stage - 1) / stage);
-        // (32x6144x4096, 48 tiles: 4 and 5 splits 8.6 and 9.1 us, 6, which do not
-        // all fit, 15.0)
+        // (32x6144x4096, 48 tiles: 4 and 5 splits 7.3 and 7.9 us, 6, which do not
+        // all fit, 12.6)
         if (splits == 1 || resident_clusters(d, splits) * (whole ? 1 : 2) >= tiles) break;
     }
     // The call's time, to be set against the pair kernel's: a fixed part (the
@@ -354,10 +354,10 @@ int64_t plan_int8(const Int8Args& p, const Int8Device& d, Int8TcArgs* out, doubl
 
 // Token tile of the pair kernel, a multiple of 32: the one whose rounds of
 // the persistent grid cost least.  Below 256 tokens a round gets only a little
-// shorter, since the weights' copies bound it (one round at 4096x4096, 128 /
-// 192 / 256 tokens a tile: 13.6 / 14.6 / 16.0 us).  512x4096x4096: 128 tokens,
-// 64 tiles in one round, 14.7 us; 256 tokens 16.2.  512x11008x4096, two rounds
-// either way: 192 tokens 25.1, 256 tokens 26.0.
+// shorter, since issuing and the weights' copies bound it (512x4096x4096, one
+// round with 128 / 192 / 256 tokens a tile: 12.0 / 12.9 / 15.0 us).
+// 512x11008x4096: 128 tokens, three rounds, 25.4; 192 and 256, two, 21.7 and
+// 24.3.  2048x28672x8192: 160 / 192 / 256 tokens 365 / 359 / 323.
 int pair_tile(const Int8Args& p, const Int8Device& d, double* us) {
     const int64_t tiles_m = ((int64_t)p.M + 2 * kI8Rows - 1) / (2 * kI8Rows), pairs = d.sm_count / 2;
     int best = kI8MaxBn;
@@ -400,8 +400,8 @@ int run_pairs(const Int8Args& p, const Int8Device& d, int bn, void* stream) {
 }
 
 // The register kernel: layers that one wave holds (B200, us a call, register /
-// ring kernel: 1x4096x4096 3.8 / 6.8, 8x8192x4096 7.8 / 9.1, 16x4096x4096 5.3 /
-// 7.1; 8x11008x4096 10.8 / 10.5, 16x8192x4096 10.0 / 9.2, 1x28672x8192 39.3 /
+// ring kernel: 1x4096x4096 3.9 / 6.1, 8x8192x4096 8.0 / 8.1, 16x4096x4096 5.4 /
+// 6.3; 8x11008x4096 10.9 / 9.6, 16x8192x4096 10.1 / 8.3, 1x28672x8192 39.6 /
 // 37.8).
 bool use_mv(const Int8Args& p) {
     if (p.flags & FLUXBIN_FLAG_TEST_WAIT_TIMEOUT) return false;   // it has no waits
@@ -427,10 +427,10 @@ int run_int8(const Int8Args& p, void* stream) {
     int st = int8_device(&d);
     if (st != FLUXBIN_OK) return st;
     // The kernel whose estimated time is shorter.  Both sides measured (B200,
-    // us a call, single / pairs): 128x4096x4096 10.6 / 12.5, 192 tokens 11.6 /
-    // 12.5, 512 tokens 13.3 / 11.9; 256x8192x8192 20.6 / 20.8, 512 tokens 31.1 /
-    // 29.9; 512x4096x11008 22.6 / 22.8, 640 tokens 29.2 / 24.6; 160x28672x8192
-    // 46.5 / 48.6, 176 tokens 67.7 / 50.5; 128x2048x2048 8.6 / 8.0.
+    // us a call, single / pairs): 128x4096x4096 12.4 / 14.3, 512 tokens 14.3 /
+    // 12.9; 256x8192x8192 21.6 / 20.9, 512 tokens 29.2 / 27.4; 512x4096x11008
+    // 22.8 / 24.1, 640 tokens 29.1 / 24.6; 160x28672x8192 46.7 / 50.9, 176 tokens
+    // 57.1 / 52.7; 128x2048x2048 9.3 / 8.6.
     double us_single = 0., us_pairs = 0.;
     Int8TcArgs a = {};
     a.p = p;

@@ -2,19 +2,19 @@
 //
 //   acc[m][t] = sum_n wq[m][n] xq[t][n],  y[t][m] (+)= acc * (sx[t] * sw[m])
 //
-// The weights are the matrix instruction's A operand (128 channels a tile, so
-// channels lie along the tensor memory's lanes and a warp stores 32
-// consecutive channels of a token at once) and the tokens its B operand: a
-// tile of `bn` tokens, a multiple of 16 up to 256, fits the batch at hand
-// without wasting operand loads on padding.  Both are K-major rows of codes,
+// The weights are the matrix instruction's A operand (128 channels a tile,
+// along the tensor memory's lanes) and the tokens its B operand: a tile of `bn`
+// tokens, a multiple of 16 up to 256, fits the batch at hand without wasting
+// operand loads on padding.  Both are K-major rows of codes,
 // copied by TMA with the 128-byte swizzle, 128 codes of K a stage; rows and
 // codes beyond the arrays' ends arrive as zeros.
 //
 // Split of K: with few tiles the stages of a tile are shared out over the
 // CTAs of a cluster.  Every CTA leaves its partial sums in its own shared
 // memory, and each then adds its share of the tokens over all of them through
-// distributed shared memory: integer sums, so the split changes no bit.  A
-// CTA releases its tensor memory before it waits for the others (none holds
+// distributed shared memory: integer sums, so the split changes no bit.  (That
+// memory yields 8 to 16 bytes per clock and SM: 2.5 us of 333x4096x11008's 18.
+// Sending the sums with st.async instead took longer, 21.)  A CTA releases its tensor memory before it waits for the others (none holds
 // tensor memory while it waits for one that may be waiting for some).
 //
 // Roles: one thread of warp 0 issues the copies, one of warp 1 the matrix
@@ -22,6 +22,11 @@
 // them.  All eight warps then empty the accumulators.  Every wait is bounded:
 // one that gives up sets bit 0 of the device error word, and the CTA's sums
 // are replaced by NaN outputs.
+//
+// Bound: for few tokens by HBM (1x28672x8192 38.0 us, 95% of the measured copy
+// rate), below that by the latency of one wave and the clusters' meeting
+// (128x4096x4096 9.0 us), then by the products (333x4096x11008: a stage takes
+// 460 clocks, 352 of them products).
 #pragma once
 
 #include <cuda.h>

@@ -31,6 +31,11 @@
 // neighbouring threads' elements (an SM gets a store away every 13 to 20
 // clocks, however narrow it is); only the ends of such a row go element by
 // element.
+// Measured (B200, a graph of calls on rotated inputs): norm with residual
+// 2048x8192 fp16 21 us, 85% of the measured copy rate, 2047x4099 24.5 (37%);
+// quant 4096x8192 19.7 (78%), 4096x8191 31 (50%); gate 2048x11008 24 (71%),
+// 2048x28672 70 (65%; 56 us without the exponential: an SM holds two such rows,
+// whose load, exponential and store phases overlap too little).
 #pragma once
 
 #include <cuda_bf16.h>
