@@ -90,7 +90,8 @@ def test_every_batch_size(T, M, N):
 @pytest.mark.parametrize("T,M,N", [
     (1, 1, 1), (1, 1, 16), (2, 3, 5), (1, 7, 15), (1, 16, 17), (3, 15, 31), (4, 17, 127), (7, 127, 129), (9, 129, 255),
     (1, 4096, 4096), (1, 1003, 2050), (4, 11008, 4096), (16, 4096, 11008), (1, 64, 65536), (5, 40, 131071), (70, 40, 131071),
-    (20, 4096, 4096), (64, 2048, 4096), (77, 1003, 2050), (333, 1024, 3000), (500, 3001, 777), (1000, 512, 64), (2049, 300, 200)])
+    (20, 4096, 4096), (64, 2048, 4096), (77, 1003, 2050), (333, 1024, 3000), (500, 3001, 777), (1000, 512, 64), (2049, 300, 200),
+    (40, 19500, 300), (24, 19001, 640), (60, 40000, 130)])
 @pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
 def test_shapes_and_types(T, M, N, kind):
     layer, rows, want = problem(T, M, N, seed=1, extra=32)
@@ -157,6 +158,24 @@ def test_empty_calls():
     y = torch.zeros(0, 64, device="cuda")
     layer.linear(rows.rows(0), y)
     fluxbin.Int8Layer(layer.w[:0], layer.scale[:0]).linear(rows, torch.zeros(4, 0, device="cuda"))
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp32"])
+@pytest.mark.parametrize("T,M,N", [(33, 19456, 256), (50, 19203, 384), (300, 149, 2000), (17, 640, 9000)])
+def test_accumulation_into_any_rows(T, M, N, kind):
+    """y's rows at every offset from a 16-byte boundary, accumulated."""
+    layer, rows, want = problem(T, M, N, seed=11)
+    if kind == "fp16":
+        layer.scale.mul_(2.0 ** -6)
+        want = want * 2.0 ** -6
+    for first in range(0, 8 if kind == "fp16" else 4):
+        buf = torch.full((T, M + 8), 5.0, dtype=DT[kind], device="cuda")
+        y = buf[:, first:first + M]
+        y.copy_(torch.randn(T, M, device="cuda"))
+        y0 = y.float().cpu().numpy().astype(np.float64)
+        layer.linear(rows, y, fluxbin.FLAG_ACCUMULATE)
+        check(y, want, kind, y0)
+        assert bool((buf[:, :first] == 5).all()) and bool((buf[:, first + M:] == 5).all())
 
 
 def test_unaligned_y():

@@ -201,6 +201,26 @@ def test_strided_and_unaligned_rows(N):
     assert torch.equal(out[:, 2:2 + N], xd[:, 3:]) and bool((out[:, :2] == 7).all()) and bool((out[:, 2 + N:] == 7).all())
 
 
+@pytest.mark.parametrize("kind,hkind", [("fp16", "fp16"), ("bf16", "fp32")])
+@pytest.mark.parametrize("N", [5, 40, 515, 2050, 9001, 33001])
+def test_every_array_at_its_own_offset(N, kind, hkind):
+    """h, delta, gamma and h_out each at another offset from a 16-byte boundary."""
+    g = np.random.default_rng([8, N])
+    T, W = 3, N + 8
+    for a, b, c, d in ((1, 2, 3, 0), (0, 1, 5, 2), (3, 0, 0, 1), (2, 7, 6, 3)):
+        h, hd = values(g, T, W, hkind, 2.0)
+        dl, dd = values(g, T, W, kind)
+        gm, gd = values(g, 1, W, kind)
+        out = torch.full((T, W), 7.0, dtype=DT[hkind], device="cuda")
+        rows, buf, sc = rows_with_guard(T, N)
+        rows.rmsnorm(hd[:, a:a + N], gd[0, c:c + N], 1e-5, delta=dd[:, b:b + N], h_out=out[:, d:d + N])
+        want, q, _ = ref.rmsnorm(h[:, a:a + N], dl[:, b:b + N], gm[0, c:c + N], 1e-5, hkind)
+        assert np.array_equal(out[:, d:d + N].float().cpu().numpy(), want.astype(np.float32))
+        assert bool((out[:, :d] == 7).all()) and bool((out[:, d + N:] == 7).all())
+        assert np.array_equal(rows.q.cpu().numpy(), q)
+        check_guard(buf, sc, T, N)
+
+
 def test_empty_rows():
     rows = fluxbin.QuantRows.empty(3, 0)
     rows.scale.fill_(7)
