@@ -127,7 +127,7 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     // threads or more (gate 1x11008: four CTAs 2.2, one with two vectors 2.6;
     // norm 1x4096: one CTA 2.1, two 2.5).  Many rows: four vectors, so that
     // several CTAs of an SM are in different phases (quant 4096x8192 1 / 2 / 4
-    // vectors 31 / 22 / 19.6, norm 2048x8192 27.4 / 22.4 / 21.0), but two for
+    // vectors 31 / 22 / 18.9, norm 2048x8192 27.4 / 22.4 / 21.0), but two for
     // the gate, a 32-bit stream and unaligned rows, which need more registers
     // (gate 2048x11008 24.3 / 26.8, norm of a 32-bit 2048x8192 32.3 / 32.8).
     const int64_t vecs = (N + 7) / 8;

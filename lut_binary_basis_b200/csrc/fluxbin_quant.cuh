@@ -33,7 +33,7 @@
 // element.
 // Measured (B200, a graph of calls on rotated inputs): norm with residual
 // 2048x8192 fp16 21 us, 85% of the measured copy rate, 2047x4099 24.5 (37%);
-// quant 4096x8192 19.7 (78%), 4096x8191 31 (50%); gate 2048x11008 24 (71%),
+// quant 4096x8192 18.9 (82%), 4096x8191 31 (50%); gate 2048x11008 24 (71%),
 // 2048x28672 70 (65%; 56 us without the exponential: an SM holds two such rows,
 // whose load, exponential and store phases overlap too little).
 #pragma once
@@ -335,9 +335,12 @@ __host__ __device__ constexpr int quant_max_threads(int vpt) { return vpt <= 1 ?
 constexpr int kQuantMaxParts = 8;   // a portable cluster: 8 * 512 threads * 4 * 8 elements hold the longest row
 
 // blockDim = (threads of a row, rows of the CTA); threads of a row a multiple
-// of 32; one row per cluster where p.parts > 1.
+// of 32; one row per cluster where p.parts > 1.  (Named one CTA per SM as the
+// least, the compiler gives the plain quantiser a few registers more: 4096x8192
+// 19.7 -> 18.9 us; the norm lost by it, 21.1 -> 22.2.)
 template <int KIND, typename E, typename H, int VPT, bool VEC>
-__global__ void __launch_bounds__(quant_max_threads(VPT)) fluxbin_quant_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(quant_max_threads(VPT), KIND == kQuantQuant ? 1 : 0)
+    fluxbin_quant_kernel(const QuantArgs p) {
     __shared__ float s_sum[32];
     __shared__ unsigned int s_max[32];
     __shared__ float s_part_sum[kQuantMaxParts];
