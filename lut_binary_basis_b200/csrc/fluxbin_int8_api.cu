@@ -399,13 +399,17 @@ int run_pairs(const Int8Args& p, const Int8Device& d, int bn, void* stream) {
                   stream, mw, mx, my, a);
 }
 
-// The register kernel: layers that one wave holds (B200, us a call, register /
-// ring kernel: 1x4096x4096 3.9 / 6.1, 8x8192x4096 8.0 / 8.1, 16x4096x4096 5.4 /
-// 6.3; 8x11008x4096 10.9 / 9.6, 16x8192x4096 10.1 / 8.3, 1x28672x8192 39.6 /
-// 37.8).
+// The register kernel: layers of which one wave of its CTAs (two per SM) holds
+// all channels and whose K its warps take in one go, or for 8 tokens in two
+// (B200, us a call, register / ring kernel; 1 token: 512x4096 2.1 / 3.9,
+// 4096x4096 3.9 / 6.0, 4736x8192 8.7 / 8.7, 6976x512 5.0 / 3.7, 2048x16384
+// 10.2 / 9.5; 16 tokens: 512x4096 3.1 / 4.2, 4096x4096 5.6 / 6.2, 2048x8192
+// 8.5 / 6.6, 6976x4096 10.2 / 7.5).
+constexpr int32_t kMvMaxRows = 296 * kMvRows;
+constexpr int32_t kMvPass = kMvWarps * kMvBatch * kMvSegment;
 bool use_mv(const Int8Args& p) {
     if (p.flags & FLUXBIN_FLAG_TEST_WAIT_TIMEOUT) return false;   // it has no waits
-    return p.T <= 2 * kMvTokens && (int64_t)p.M * p.N <= ((int64_t)1 << (p.T <= kMvTokens ? 25 : 24));
+    return p.T <= 2 * kMvTokens && p.M <= kMvMaxRows && p.N <= (p.T <= kMvTokens ? 2 : 1) * kMvPass;
 }
 
 int run_int8(const Int8Args& p, void* stream) {

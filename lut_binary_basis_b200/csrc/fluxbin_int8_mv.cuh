@@ -37,10 +37,16 @@ __device__ __forceinline__ uint4 mv_load(const int8_t* row, int n, int N) {
         else
             v = *reinterpret_cast<const uint4*>(row + n);
     } else if (n < N) {
-        uint32_t w[4] = {0, 0, 0, 0};
+        // whole words, then the bytes of the last one (every load before its use)
+        uint32_t w[4], b[3];
+        const int words = (N - n) / 4, bytes = (N - n) % 4;
 #pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (n + i < N) w[i / 4] |= (uint32_t)(uint8_t)row[n + i] << (8 * (i % 4));
+        for (int k = 0; k < 4; ++k) w[k] = k < words ? *reinterpret_cast<const uint32_t*>(row + n + 4 * k) : 0u;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) b[k] = k < bytes ? (uint32_t)(uint8_t)row[n + 4 * words + k] : 0u;
+        const uint32_t last = b[0] | (b[1] << 8) | (b[2] << 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] |= k == words ? last : 0u;
         v = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return v;
@@ -55,7 +61,7 @@ __device__ __forceinline__ void mv_mma(int (&c)[4], uint32_t a0, uint32_t a1, ui
 }
 
 template <typename Y, bool ACC, int NT>
-__global__ void __launch_bounds__(32 * kMvWarps) fluxbin_int8_mv_kernel(const Int8Args p) {
+__global__ void __launch_bounds__(32 * kMvWarps, 2) fluxbin_int8_mv_kernel(const Int8Args p) {
     __shared__ int part[kMvWarps][NT * kMvTokens][kMvRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, q = lane & 3;         // row (and row + 8) or token; 16 codes of a segment

@@ -89,7 +89,7 @@ def test_every_batch_size(T, M, N):
 
 @pytest.mark.parametrize("T,M,N", [
     (1, 1, 1), (1, 1, 16), (2, 3, 5), (1, 7, 15), (1, 16, 17), (3, 15, 31), (4, 17, 127), (7, 127, 129), (9, 129, 255),
-    (1, 4096, 4096), (1, 1003, 2050), (4, 11008, 4096), (16, 4096, 11008), (1, 64, 65536), (5, 40, 131071), (70, 40, 131071),
+    (1, 4096, 4096), (1, 1003, 2050), (3, 4736, 8192), (2, 4737, 300), (16, 4736, 4096), (9, 500, 4097), (8, 300, 8193), (4, 11008, 4096), (16, 4096, 11008), (1, 64, 65536), (5, 40, 131071), (70, 40, 131071),
     (20, 4096, 4096), (64, 2048, 4096), (77, 1003, 2050), (333, 1024, 3000), (500, 3001, 777), (1000, 512, 64), (2049, 300, 200),
     (40, 19500, 300), (24, 19001, 640), (60, 40000, 130)])
 @pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
