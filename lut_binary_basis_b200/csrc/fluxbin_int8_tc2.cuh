@@ -105,6 +105,98 @@ __device__ __forceinline__ void int8_ld(uint32_t taddr, int (&v)[C]) {
     else int8_ld16(taddr, v);
 }
 
+// Accumulation into a tile of y whose rows TMA cannot move, by one group: its
+// chunks of 16 tokens (every other one) through an fp32 staging buffer, 128
+// channels a token with a gap after every 8, so that lanes which read 8 channels
+// each meet different banks.  A lane adds and writes the 16 bytes of a row that
+// start on a 16-byte boundary, requested two chunks ahead (a chunk takes less
+// time than a load); the ends of a row go element by element.  Against reading
+// and writing a whole chunk at a time: 495x22306x1152 fp32 65 -> 39.5 us,
+// 2000x11009x1000 bf16 73 -> 51; with one chunk ahead 49 and 60; without
+// accumulation the same way costs 5% more than int8_rows_out.  `ready` waits for
+// the tile's accumulators and scales and says whether they are right.
+constexpr int kI8RowsPitch = kI8Rows + kI8Rows / 8;
+__device__ __forceinline__ uint32_t int8_rows_at(uint32_t buf, int j, int ch) {
+    return buf + (uint32_t)(4 * (j * kI8RowsPitch + ch + (ch >> 3)));
+}
+
+template <typename Y, typename READY>
+__device__ __forceinline__ void int8_pair_rows_add(const Int8Args& p, uint32_t acc, uint32_t buf, uint32_t sx, float sw,
+                                                   int64_t t0, int m0, int chunks, int group, int e, int row, READY ready) {
+    constexpr int kPer = 16 / (int)sizeof(Y), kLanes = kI8Rows / kPer, kStep = 128 / kLanes, S = 16 / kStep;
+    static_assert(16 * kI8RowsPitch * 4 <= 2 * kI8PairOutBytes, "a group's two staging buffers");
+    const int l = e % kLanes, j0 = e / kLanes, nv = p.M - m0 < kI8Rows ? p.M - m0 : kI8Rows;
+    // this lane's 16 bytes of token j start at element c, and it also has
+    // element `end` (-1: none)
+    struct Place { Y* y; int c, end; };
+    const auto place = [&](int64_t t) {
+        Place r;
+        r.y = static_cast<Y*>(p.y) + t * p.ldy + m0;
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(r.y) & 15u;
+        const int head = off ? (int)((16u - off) / sizeof(Y)) : 0;
+        const int whole = nv > head ? (nv - head) / kPer : 0;
+        r.c = t < p.T && l < whole ? head + l * kPer : -1;
+        r.end = l < head ? l : whole * kPer + l;
+        if (t >= p.T || l >= 2 * kPer || r.end >= nv) r.end = -1;
+        return r;
+    };
+    struct Held { uint4 v[S]; Y end[S]; };
+    const auto request = [&](int q, Held& h) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const Place r = place(t0 + 16 * q + j0 + s * kStep);
+            if (r.c >= 0) h.v[s] = *reinterpret_cast<const uint4*>(r.y + r.c);
+            if (r.end >= 0) h.end[s] = r.y[r.end];
+        }
+    };
+    bool ok = true;
+    const auto add = [&](int q, Held& h) {
+        int v[16];
+        int8_ld16(acc + (uint32_t)(16 * q), v);
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const float4 s4 = smem_at<const float4>(sx + (uint32_t)(4 * (16 * q + j)));
+            f[j] = s4.x;
+            f[j + 1] = s4.y;
+            f[j + 2] = s4.z;
+            f[j + 3] = s4.w;
+        }
+        tc_wait_ld();
+        int8_out_sync(group);                      // the chunk before has been read
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float x = int8_value(v[j], f[j], sw);
+            smem_at<float>(int8_rows_at(buf, j, row)) = ok ? x : __int_as_float(0x7fc00000);
+        }
+        int8_out_sync(group);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int j = j0 + s * kStep;
+            const Place r = place(t0 + 16 * q + j);
+            if (r.c >= 0) {
+                alignas(16) Y o[kPer];
+                *reinterpret_cast<uint4*>(o) = h.v[s];
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+                    o[k] = from_f32<Y>(to_f32(o[k]) + smem_at<const float>(int8_rows_at(buf, j, r.c + k)));
+                *reinterpret_cast<uint4*>(r.y + r.c) = *reinterpret_cast<const uint4*>(o);
+            }
+            if (r.end >= 0)
+                r.y[r.end] = from_f32<Y>(to_f32(h.end[s]) + smem_at<const float>(int8_rows_at(buf, j, r.end)));
+        }
+        if (q + 4 < chunks) request(q + 4, h);
+    };
+    Held h0, h1;
+    if (group < chunks) request(group, h0);
+    if (group + 2 < chunks) request(group + 2, h1);
+    ok = ready();
+    for (int q = group; q < chunks; q += 4) {
+        add(q, h0);
+        if (q + 2 < chunks) add(q + 2, h1);
+    }
+}
+
 struct Int8PairTile {
     int tm, tt;
 };
@@ -274,7 +366,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 const int c = tid - 64;
                 smem_at<float>(kI8PairSxOff + (b * kI8MaxBn + c) * 4) = c < a.bn && t0 + c < p.T ? __ldg(p.sx + t0 + c) : 0.f;
             }
-            if (ACC && !bulk && tid - 64 < a.bn && t0 + tid - 64 < p.T) int8_prefetch_row<Y>(p, t0 + tid - 64, m0);
             if (ACC) {                             // (the tile before may have gone out by plain stores)
                 fence_async_smem();
                 int8_out_sync(group);
@@ -283,12 +374,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 load_y(group);
             }
-            if (ok) ok = tc_mbar_wait(acc_full0 + 8 * b, (uint32_t)(n >> 1) & 1u, a.spin_limit);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-            int8_out_sync_all();                   // the token scales are in place
             const uint32_t acc = tmem + (uint32_t)(b * kI8MaxBn) + ((uint32_t)(quarter * 32) << 16);
-            for (int q = group; q < chunks; q += 2) {
+            const auto ready = [&]() {
+                if (ok) ok = tc_mbar_wait(acc_full0 + 8 * b, (uint32_t)(n >> 1) & 1u, a.spin_limit);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                int8_out_sync_all();               // the token scales are in place
+                return ok;
+            };
+            if (ACC && !bulk) {
+                if (e == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                int8_pair_rows_add<Y>(p, acc, buf0, (uint32_t)(kI8PairSxOff + b * kI8MaxBn * 4), sw, t0, m0, a.bn / 16,
+                                      group, e, row, ready);
+            } else {
+                ready();
+            }
+            for (int q = group; q < chunks && (!ACC || bulk); q += 2) {
                 const int k = (q >> 1) & 1, c = q * C;
                 const uint32_t out = buf0 + (uint32_t)(k * kI8PairOutBytes);
                 int v[C];
@@ -296,23 +397,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 // the staging buffer is free once what went out of it two
                 // chunks ago has been read; with accumulation the next chunk's
                 // y is requested a chunk ahead
-                if (bulk) {
-                    if (e == 0) {
-                        if (ACC) {
-                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                            if (q + 2 < chunks) load_y(q + 2);
-                        } else {
-                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        }
+                if (e == 0) {
+                    if (ACC) {
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        if (q + 2 < chunks) load_y(q + 2);
+                    } else if (bulk) {
+                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    } else {
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
-                } else if (e == 0) {
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 }
-                if (!ACC || !bulk) int8_out_sync(group);
-                if (ACC && !bulk) {
-                    int8_rows_in<Y, 128, 2>(p, out, t0 + c, C, m0, e);
-                    int8_out_sync(group);
-                }
+                if (!ACC) int8_out_sync(group);
                 float f[C];
 #pragma unroll
                 for (int j = 0; j < C; j += 4) {
@@ -328,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                     f[j] = int8_value(v[j], f[j], sw);
                     if (!ok) f[j] = __int_as_float(0x7fc00000);
                 }
-                if (ACC && bulk) {
+                if (ACC) {
                     ok = tc_mbar_wait(y_full + 8 * k, (y_parity >> k) & 1u, kI8SpinLimit) && ok;
                     y_parity ^= 1u << k;
                 }
@@ -337,9 +432,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                     Y& o = smem_at<Y>(out + (uint32_t)((j * kI8Rows + row) * (int)sizeof(Y)));
                     o = from_f32<Y>(ACC ? to_f32(o) + f[j] : f[j]);
                 }
-                if (bulk) fence_async_smem();
+                if (ACC || bulk) fence_async_smem();
                 int8_out_sync(group);
-                if (bulk) {
+                if (ACC || bulk) {
                     if (e == 0) {
                         if (t0 + c < p.T && m0 < p.M)
                             asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
