@@ -145,6 +145,15 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     const int tpr = std::max(32, (int)(((vecs + per_thread - 1) / per_thread + 31) / 32 * 32));
     a.parts = parts;
     const int rpc = tpr >= 128 ? 1 : 128 / tpr;
+    // Rows from a CTA's own to the one that it asks L2 for, so that memory is
+    // busy while the CTAs at work compute and store: about half of those that
+    // fit the GPU at a time, for CTAs do not start all at once (quant 4096x8192
+    // 0 / 1/4 / 1/2 / 1 of them ahead 18.9 / 18.1 / 17.0 / 16.8 us, 32-bit norm
+    // 2048x8192 32.5 / 30.4 / 30.4 / 32.1).  The gate gains where a cluster has
+    // the row or rows are unaligned (2048x28672 68 -> 63.8, 2048x28671
+    // 122 -> 98) and loses a little elsewhere (2048x4096 9.8 -> 10.4).
+    const int64_t resident = (vpt == 1 ? 2048 : vpt == 2 ? 1536 : 1024) / (tpr * rpc) * kQuantFewBlocks / parts;
+    if (KIND != kQuantSilu || parts > 1 || !vec) a.ahead = (int)((resident + 1) / 2) * rpc;
     const bool bf = (flags & FLUXBIN_FLAG_BF16) != 0;
     QuantFn fn;
     if constexpr (KIND == kQuantNorm) {

@@ -31,11 +31,13 @@
 // neighbouring threads' elements (an SM gets a store away every 13 to 20
 // clocks, however narrow it is); only the ends of such a row go element by
 // element.
+// A CTA also asks L2 for the inputs of a row that will start later, so that
+// memory stays busy while the resident CTAs compute and store.
 // Measured (B200, a graph of calls on rotated inputs): norm with residual
-// 2048x8192 fp16 21 us, 85% of the measured copy rate, 2047x4099 24.5 (37%);
-// quant 4096x8192 18.9 (82%), 4096x8191 31 (50%); gate 2048x11008 24 (71%),
-// 2048x28672 70 (65%; 56 us without the exponential: an SM holds two such rows,
-// whose load, exponential and store phases overlap too little).
+// 2048x8192 fp16 20 us, 89% of the measured copy rate, 2047x4099 22 (41%);
+// quant 4096x8192 17.0 (91%), 4096x8191 33 (47%); gate 2048x11008 24 (71%),
+// 2048x28672 64 (70%: the exponential's and the reciprocal's unit is busy 1.9 us
+// of the 4.6 that an SM takes for such a row).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -59,6 +61,7 @@ struct QuantArgs {
     int32_t T, N;
     float eps;
     int32_t parts;        // CTAs (of one cluster) that share a row
+    int32_t ahead;        // rows from here to the one whose inputs this CTA asks L2 for (0: none)
 };
 
 // --- pairs of fp32 (one instruction for both) -------------------------------
@@ -268,6 +271,29 @@ __device__ __forceinline__ void quant_inputs(const QuantArgs& p, int64_t t, int 
         x.b = quant_load<VEC>(static_cast<const E*>(p.b) + t * p.ldb, n, p.N);
 }
 
+// Asks L2 for elements n .. n+count-1 of a row of N, as far as they are whole
+// 16-byte units.
+template <typename T>
+__device__ __forceinline__ void quant_prefetch(const T* row, int n, int count, int N) {
+    const int c = min(count, N - n);
+    if (c <= 0) return;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + n), from = (at + 15u) & ~(uintptr_t)15u;
+    const uintptr_t end = (at + (uintptr_t)c * sizeof(T)) & ~(uintptr_t)15u;
+    if (from < end)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(end - from)) : "memory");
+}
+
+// Asks for the inputs of the row `ahead` rows on, which a CTA that has not
+// started yet will read (one thread).
+template <int KIND, typename E, typename H>
+__device__ __forceinline__ void quant_prefetch_ahead(const QuantArgs& p, int64_t t, int n, int count) {
+    if (threadIdx.x != 0 || p.ahead == 0 || t + p.ahead >= p.T) return;
+    t += p.ahead;
+    quant_prefetch(static_cast<const H*>(p.a) + t * p.lda, n, count, p.N);
+    if (KIND == kQuantSilu || (KIND == kQuantNorm && p.b))
+        quant_prefetch(static_cast<const E*>(p.b) + t * p.ldb, n, count, p.N);
+}
+
 // The row's values before its common factor; their largest magnitude, and for
 // rmsnorm h' (written) and the sum of its squares.
 template <int KIND, typename E, typename H, bool VEC>
@@ -359,10 +385,15 @@ __global__ void __launch_bounds__(quant_max_threads(VPT), KIND == kQuantQuant ? 
     float mxf = 0.f;
     uint64_t v[VPT][4];
     if (live) {
+        // what is asked for ahead comes after the own loads, but in the gate
+        // before them: there it costs registers after them (2048x28672 63.8
+        // against 66.5 us; norm of a 32-bit 2048x8192 31.4 against 30.4)
+        if (KIND == kQuantSilu) quant_prefetch_ahead<KIND, E, H>(p, t, n0, 8 * VPT * tpr);
         // every load before the first store
         QuantIn<KIND, E, H> x[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) quant_inputs<KIND, E, H, VEC>(p, t, n0 + 8 * i * tpr, x[i]);
+        if (KIND != kQuantSilu) quant_prefetch_ahead<KIND, E, H>(p, t, n0, 8 * VPT * tpr);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) quant_values<KIND, E, H, VEC>(p, t, n0 + 8 * i * tpr, x[i], v[i], ss2, mxf);
     }
