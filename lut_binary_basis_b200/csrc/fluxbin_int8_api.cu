@@ -65,6 +65,18 @@ int launch(K kernel, dim3 grid, dim3 block, size_t smem, int cluster, void* stre
     return e == cudaSuccess ? FLUXBIN_OK : report_cuda_failure(e);
 }
 
+constexpr int kMaxDevices = 64;
+std::mutex g_int8_mu;
+
+struct Int8Device {
+    bool ready = false;
+    int index = 0;
+    int sm_count = 0;
+    unsigned int* err = nullptr;
+} g_int8_dev[kMaxDevices];
+
+int int8_device(Int8Device* out);
+
 using QuantFn = void (*)(QuantArgs);
 
 constexpr int64_t kQuantFewBlocks = 148;                 // CTAs that have an SM each
@@ -80,6 +92,35 @@ QuantFn pick_quant(int vpt) {
 }
 template <int KIND, typename E, typename H>
 QuantFn pick_quant(int vpt, bool vec) { return vec ? pick_quant<KIND, E, H, true>(vpt) : pick_quant<KIND, E, H, false>(vpt); }
+
+template <typename E>
+QuantFn pick_gate(int vpt) {
+    return vpt == 2   ? &fluxbin_gate_rows_kernel<E, 2>
+           : vpt == 3 ? &fluxbin_gate_rows_kernel<E, 3>
+                      : &fluxbin_gate_rows_kernel<E, kGateMaxVpt>;
+}
+
+// The gate for many aligned rows: vectors a thread, threads and CTAs per SM, or
+// 0 vectors where the other kernel has it.  Rows of up to 1536 vectors: as many
+// CTAs of up to 512 threads as an SM's registers hold, for they hide each
+// other's reductions (2048x11008: two CTAs with 3 vectors 22.1 us, with 4 22.7,
+// one with 2 23.6; 2048x8192 16.3); longer ones a CTA with the fewest vectors
+// (2048x14336: 2 vectors 27.3, 3 28.4, two CTAs with 4 28.6).  The other kernel
+// takes 24.7, 18.0, 31.0 and, at 2048x28672, 64.4 for 51.7.  A CTA should have
+// four rows, two where the other kernel needs a cluster for one (296x14336 6.1
+// against 6.6 here, 592 rows 10.8 and 10.1; 296x20480 11.7 and 8.5).
+struct GatePlan { int vpt, threads, per_sm; };
+GatePlan plan_gate(int64_t T, int64_t N) {
+    GatePlan g = {0, 0, 1};
+    const int64_t vecs = N / 8;
+    if (vecs < 512 || vecs * 64 > kGateMaxSmem) return g;
+    const int64_t most = vecs <= 3 * 512 ? 512 : kGateMaxThreads;
+    const int vpt = std::max(2, (int)((vecs + most - 1) / most));
+    g.threads = (int)(((vecs + vpt - 1) / vpt + 31) / 32 * 32);
+    g.per_sm = kGateMaxThreads / g.threads;
+    if (T >= (vecs > 2048 ? 2 : 4) * kQuantFewBlocks * g.per_sm) g.vpt = vpt;
+    return g;
+}
 
 // Checks what the three operators share and launches.  `in0`, `in1` (delta or
 // up, may be null), `gamma` and `h_out` as the operator has them.
@@ -122,6 +163,17 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     a.eps = eps;
     const bool vec = N % 8 == 0 && in0.rows_aligned16() && (!in1.p || in1.rows_aligned16()) &&
                      (!gamma || ptr_aligned(gamma, 16)) && (!h_out.p || h_out.rows_aligned16());
+    if (KIND == kQuantSilu && vec) {
+        const GatePlan g = plan_gate(T, N);
+        if (g.vpt) {
+            Int8Device d;
+            const int st = int8_device(&d);
+            if (st != FLUXBIN_OK) return st;
+            const QuantFn fn = (flags & FLUXBIN_FLAG_BF16) ? pick_gate<__nv_bfloat16>(g.vpt) : pick_gate<__half>(g.vpt);
+            return launch(fn, dim3((unsigned)std::min<int64_t>(T, (int64_t)d.sm_count * g.per_sm)), dim3((unsigned)g.threads),
+                          (size_t)N * 8, 1, stream, a);
+        }
+    }
     // Vectors of 8 elements a thread, and CTAs a row (B200, us a call, a graph
     // of calls).  Few rows: one vector, and a cluster once it leaves a CTA 256
     // threads or more (gate 1x11008: four CTAs 2.2, one with two vectors 2.6;
@@ -150,7 +202,7 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
     // fit the GPU at a time, for CTAs do not start all at once (quant 4096x8192
     // 0 / 1/4 / 1/2 / 1 of them ahead 18.9 / 18.1 / 17.0 / 16.8 us, 32-bit norm
     // 2048x8192 32.5 / 30.4 / 30.4 / 32.1).  The gate gains where a cluster has
-    // the row or rows are unaligned (2048x28672 68 -> 63.8, 2048x28671
+    // the row or rows are unaligned (2048x29000 71 -> 67, 2048x28671
     // 122 -> 98) and loses a little elsewhere (2048x4096 9.8 -> 10.4).
     const int64_t resident = (vpt == 1 ? 2048 : vpt == 2 ? 1536 : 1024) / (tpr * rpc) * kQuantFewBlocks / parts;
     if (KIND != kQuantSilu || parts > 1 || !vec) a.ahead = (int)((resident + 1) / 2) * rpc;
@@ -173,16 +225,6 @@ int run_quant(const Rows& in0, const Rows& in1, const void* gamma, float eps, co
 // ---------------------------------------------------------------------------
 // The integer product
 // ---------------------------------------------------------------------------
-
-constexpr int kMaxDevices = 64;
-std::mutex g_int8_mu;
-
-struct Int8Device {
-    bool ready = false;
-    int index = 0;
-    int sm_count = 0;
-    unsigned int* err = nullptr;
-} g_int8_dev[kMaxDevices];
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -215,8 +257,8 @@ Int8EmptyFn pick_empty(bool acc) { return acc ? &fluxbin_int8_empty_kernel<Y, tr
 
 constexpr int kI8MaxSmem = 227 * 1024;
 
-// Per-device set-up of the product's kernels: the error word, the number of
-// SMs, the opt-in to their shared memory; once the tensor-map encoder.
+// Per-device set-up: the product's error word, the number of SMs, the kernels'
+// opt-in to their shared memory; once the tensor-map encoder.
 int int8_device(Int8Device* out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -241,6 +283,10 @@ int int8_device(Int8Device* out) {
                                               kI8MaxSmem)) != cudaSuccess ||
                     (e = cudaFuncSetAttribute(pick_int8_pair(f | acc), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               kI8PairSmem)) != cudaSuccess)
+                    return report_cuda_failure(e);
+        for (int vpt = 2; vpt <= kGateMaxVpt; ++vpt)
+            for (const QuantFn fn : {pick_gate<__half>(vpt), pick_gate<__nv_bfloat16>(vpt)})
+                if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGateMaxSmem)) != cudaSuccess)
                     return report_cuda_failure(e);
         const int st = device_error_word(dev, &d.err);
         if (st != FLUXBIN_OK) return st;

@@ -35,9 +35,8 @@
 // memory stays busy while the resident CTAs compute and store.
 // Measured (B200, a graph of calls on rotated inputs): norm with residual
 // 2048x8192 fp16 20 us, 89% of the measured copy rate, 2047x4099 22 (41%);
-// quant 4096x8192 17.0 (91%), 4096x8191 33 (47%); gate 2048x11008 24 (71%),
-// 2048x28672 64 (70%: the exponential's and the reciprocal's unit is busy 1.9 us
-// of the 4.6 that an SM takes for such a row).
+// quant 4096x8192 17.0 (91%), 4096x8191 33 (47%); gate 2048x11008 22.5 (77%),
+// 2048x28672 52 (87%), 2048x28671 98 (46%).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -323,6 +322,23 @@ __device__ __forceinline__ void quant_values(const QuantArgs& p, int64_t t, int 
     for (int k = 0; k < 4; ++k) mx = max_abs(mx, v[k]);
 }
 
+// A row's scale, from the bits of its largest magnitude and its common factor.
+struct QuantScale {
+    float s, pre, inv;
+    bool finite;
+};
+__device__ __forceinline__ QuantScale quant_scale(unsigned int mx, float factor) {
+    const float amax = __uint_as_float(mx);
+    QuantScale c;
+    c.s = amax * factor / 127.f;
+    c.finite = fabsf(c.s) < INFINITY;
+    if (!c.finite) c.s = NAN;
+    // 127 / amax, the row scaled up first where the quotient would overflow
+    c.pre = amax < 0x1p-100f ? 0x1p100f : 1.f;
+    c.inv = (c.finite && mx != 0u) ? 127.f / (amax * c.pre) : 0.f;
+    return c;
+}
+
 // Codes of a chunk: v * pre * inv is at most 127 (1 + 2^-22) in magnitude, so
 // adding 1.5 * 2^23 rounds it to the nearest integer (ties to even) and leaves
 // that integer, modulo 2^8, in the low byte.  (The addition is a scalar one:
@@ -358,6 +374,8 @@ __device__ __forceinline__ void quant_codes(const QuantArgs& p, int64_t t, int n
 // registers allow).
 __host__ __device__ constexpr int quant_max_threads(int vpt) { return vpt <= 1 ? 1024 : vpt == 2 ? 768 : 512; }
 
+constexpr int kGateMaxThreads = 1024, kGateMaxVpt = 4;
+constexpr int kGateMaxSmem = 226 * 1024;   // two rows of both inputs
 constexpr int kQuantMaxParts = 8;   // a portable cluster: 8 * 512 threads * 4 * 8 elements hold the longest row
 
 // blockDim = (threads of a row, rows of the CTA); threads of a row a multiple
@@ -439,21 +457,73 @@ __global__ void __launch_bounds__(quant_max_threads(VPT), KIND == kQuantQuant ? 
         }
     }
     if (!live) return;
-    const float amax = __uint_as_float(mx);
     float factor = 1.f;
     if constexpr (KIND == kQuantNorm) {
         factor = 1.f / sqrtf(ss / (float)p.N + p.eps);
         if (!(ss < INFINITY)) factor = NAN;
     }
-    float s = amax * factor / 127.f;
-    const bool finite = fabsf(s) < INFINITY;
-    if (!finite) s = NAN;
-    if (threadIdx.x == 0 && rank == 0) p.scale[t] = s;
-    // 127 / amax, the row scaled up first where the quotient would overflow
-    const float pre = amax < 0x1p-100f ? 0x1p100f : 1.f;
-    const float inv = (finite && mx != 0u) ? 127.f / (amax * pre) : 0.f;
+    const QuantScale c = quant_scale(mx, factor);
+    if (threadIdx.x == 0 && rank == 0) p.scale[t] = c.s;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) quant_codes(p, t, n0 + 8 * i * tpr, v[i], pre, inv, finite);
+    for (int i = 0; i < VPT; ++i) quant_codes(p, t, n0 + 8 * i * tpr, v[i], c.pre, c.inv, c.finite);
+}
+
+// The gate for many rows: a CTA takes every gridDim.x-th row, and copies the
+// next one into shared memory while it works on the current one, so that memory
+// does not wait for the exponentials and the stores (2048x28672 64 -> 52 us, of
+// 45 that memory takes; the exponential's and the reciprocal's unit is busy for
+// 26).  Each thread copies what it
+// reads itself (no barrier but the reduction's); the buffer that it copies into
+// was read a row ago, before that row's reduction.
+template <typename E, int VPT>
+__global__ void __launch_bounds__(kGateMaxThreads, 1) fluxbin_gate_rows_kernel(const QuantArgs p) {
+    extern __shared__ __align__(16) uint4 gate_rows[];          // [2][gate, up][N / 8]
+    __shared__ unsigned int s_max[2][32];
+    const int tid = (int)threadIdx.x, nt = (int)blockDim.x, lane = tid & 31, vecs = p.N / 8;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const auto request = [&](int64_t t, int s) {
+        if (t < p.T) {
+            const E* g = static_cast<const E*>(p.a) + t * p.lda;
+            const E* u = static_cast<const E*>(p.b) + t * p.ldb;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = i * nt + tid;
+                if (c < vecs) {
+                    const uint32_t to = (uint32_t)__cvta_generic_to_shared(gate_rows + 2 * s * vecs + c);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(g + 8 * c) : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * vecs), "l"(u + 8 * c) : "memory");
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int64_t t = blockIdx.x;
+    int s = 0;
+    request(t, s);
+    for (; t < p.T; t += gridDim.x, s ^= 1) {
+        request(t + gridDim.x, s ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const uint4* in = gate_rows + 2 * s * vecs;
+        uint64_t v[VPT][4], ss = 0ull;
+        float mxf = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            QuantIn<kQuantSilu, E, E> x;
+            const int c = i * nt + tid;
+            put(x.a.w, c < vecs ? in[c] : make_uint4(0, 0, 0, 0));
+            put(x.b.w, c < vecs ? in[vecs + c] : make_uint4(0, 0, 0, 0));
+            quant_values<kQuantSilu, E, E, true>(p, t, 0, x, v[i], ss, mxf);
+        }
+        unsigned int mx = __reduce_max_sync(0xffffffffu, __float_as_uint(mxf) & 0x7fffffffu);
+        if (lane == 0) s_max[s][tid >> 5] = mx;
+        __syncthreads();
+        mx = __reduce_max_sync(0xffffffffu, lane < nt / 32 ? s_max[s][lane] : 0u);
+        const QuantScale c = quant_scale(mx, 1.f);
+        if (tid == 0) p.scale[t] = c.s;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) quant_codes(p, t, (i * nt + tid) * 8, v[i], c.pre, c.inv, c.finite);
+    }
 }
 
 }  // namespace fluxbin

@@ -242,3 +242,59 @@ def test_many_rows():
     rows.quantize(x)
     q, s = ref.quant(x.float().cpu().numpy())
     assert np.array_equal(rows.q.cpu().numpy(), q) and np.array_equal(rows.scale.cpu().numpy(), s)
+
+
+def in_batches(T, N, run, batch=16):
+    """Codes and scales of the same rows, a few at a time."""
+    rows = fluxbin.QuantRows.empty(T, N)
+    for t in range(0, T, batch):
+        run(fluxbin.QuantRows(rows.q[t:t + batch], rows.scale[t:t + batch]), slice(t, t + batch))
+    return rows
+
+
+def same(a, b):
+    return torch.equal(a.q, b.q) and torch.equal(a.scale.view(torch.int32), b.scale.view(torch.int32))
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("T,N", [(2371, 4096), (1200, 8200), (1184, 12288), (593, 12296), (300, 20480), (301, 28920),
+                                 (296, 28928), (296, 28936), (297, 28671), (1700, 1000)])
+def test_gate_of_many_rows(T, N, kind):
+    """A row's codes and scale do not depend on how many rows there are, on
+    its neighbours (zeros, NaN, infinity among them) or on the kernel."""
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    gu = (torch.randn(T, 2 * N, device="cuda", generator=g) * 2).to(DT[kind])
+    gu[T // 3] = 0
+    gu[T // 2, N - 1] = float("nan")
+    gu[T // 2 + 1, N + 3] = float("inf")
+    gu[T - 1] *= 2.0 ** -6
+    rows, buf, sc = rows_with_guard(T, N)
+    rows.silu_mul(gu[:, :N], gu[:, N:])
+    few = in_batches(T, N, lambda r, at: r.silu_mul(gu[at, :N], gu[at, N:]))
+    assert same(rows, few)
+    check_guard(buf, sc, T, N)
+    assert rows.scale[T // 3].item() == 0 and bool(torch.isnan(rows.scale[T // 2:T // 2 + 2]).all())
+    assert not rows.q[T // 3].any() and not rows.q[T // 2:T // 2 + 2].any()
+    for t in (0, T // 3 + 1, T - 2, T - 1):
+        host = gu[t:t + 1].float().cpu().numpy()
+        v = ref.silu_mul(host[:, :N], host[:, N:])
+        delta = (6 + 1.173 * np.abs(host[:, :N]).max()) * 2.0 ** -23
+        a = np.abs(v).max()
+        assert abs(rows.scale[t].item() * 127.0 / a - 1) <= delta + 2.0 ** -23
+        assert np.abs(rows.q[t].cpu().numpy() - v[0] * (127 / a)).max() <= 0.5 + 127 * 2 * delta + 2.0 ** -15
+
+
+@pytest.mark.parametrize("N", [256, 4096, 8191, 28672])
+def test_many_rows_as_in_small_batches(N):
+    """What is asked of L2 ahead stays within the rows and changes nothing."""
+    T = 1500 if N < 10000 else 400
+    x = torch.randn(T, N, device="cuda").bfloat16()
+    rows = fluxbin.QuantRows.empty(T, N)
+    assert same(rows.quantize(x) or rows, in_batches(T, N, lambda r, at: r.quantize(x[at])))
+    h, gamma, h2 = torch.randn(T, N, device="cuda"), torch.rand(N, device="cuda").bfloat16(), torch.empty(T, N, device="cuda")
+    rows.rmsnorm(h, gamma, 1e-6, delta=x, h_out=h2)
+    assert torch.equal(h2, h + x.float())
+    few = in_batches(T, N, lambda r, at: r.rmsnorm(h[at], gamma, 1e-6, delta=x[at]))
+    assert torch.equal(rows.q, few.q)
+    # the sums of squares may be taken in another order: N / 32 + 16 roundings of half a step at most, each way, halved by the root
+    assert bool(((rows.scale - few.scale).abs() <= rows.scale * (N / 32 + 16) * 2.0 ** -24).all())
