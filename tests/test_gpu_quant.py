@@ -298,3 +298,30 @@ def test_many_rows_as_in_small_batches(N):
     assert torch.equal(rows.q, few.q)
     # the sums of squares may be taken in another order: N / 32 + 16 roundings of half a step at most, each way, halved by the root
     assert bool(((rows.scale - few.scale).abs() <= rows.scale * (N / 32 + 16) * 2.0 ** -24).all())
+
+
+def test_gate_of_many_rows_in_two_graphs_at_once():
+    """Captured calls that run side by side, each with its own rows, replayed
+    after the inputs have changed."""
+    T, N = 700, 16400
+    gu = [torch.randn(T, 2 * N, device="cuda").half() for _ in range(2)]
+    rows = [fluxbin.QuantRows.empty(T, N) for _ in range(2)]
+    graphs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for x, r in zip(gu, rows):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            r.silu_mul(x[:, :N], x[:, N:])
+        graphs.append(graph)
+    for _ in range(3):
+        for x in gu:
+            x.copy_(torch.randn(T, 2 * N, device="cuda"))
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x, r in zip(gu, rows):
+            want = fluxbin.QuantRows.empty(T, N)
+            want.silu_mul(x[:, :N], x[:, N:])
+            assert same(r, want)
