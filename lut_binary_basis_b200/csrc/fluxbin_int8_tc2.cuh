@@ -345,6 +345,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
         // the group's two staging buffers
         const uint32_t buf0 = (uint32_t)(kI8PairOutOff + 2 * group * kI8PairOutBytes), y_full = y_full0 + 16 * group;
         uint32_t y_parity = 0u;                    // of the loads of y into each of them (one bit each)
+        // the group's chunks take its buffers in turn, across tiles too: the wait
+        // below leaves the chunk before unread, and a tile may have an odd number
+        const int odd = ((chunks - group + 1) >> 1) & 1;
         int64_t n = 0;
         for (int64_t i = first; i < a.tiles; i += step, ++n) {
             const Int8PairTile t = int8_pair_tile(a, i);
@@ -354,9 +357,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             // TMA writes whole 16-byte pieces: a ragged last tile only where
             // M ends on one
             const bool bulk = a.bulk > (p.M - m0 >= kI8Rows ? 0 : 1);
+            const int turn = b & odd;              // the buffer of the tile's first chunk
             // requests a chunk's y (accumulation) into its staging buffer
             const auto load_y = [&](int q) {
-                const int k = (q >> 1) & 1;
+                const int k = ((q >> 1) & 1) ^ turn;
                 int8_expect(y_full + 8 * k, (uint32_t)kI8PairOutBytes);
                 int8_tma(sb + buf0 + k * kI8PairOutBytes, &map_y, m0, (int)t0 + q * C, y_full + 8 * k);
             };
@@ -390,13 +394,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 ready();
             }
             for (int q = group; q < chunks && (!ACC || bulk); q += 2) {
-                const int k = (q >> 1) & 1, c = q * C;
+                const int k = ((q >> 1) & 1) ^ turn, c = q * C;
                 const uint32_t out = buf0 + (uint32_t)(k * kI8PairOutBytes);
                 int v[C];
                 int8_ld<C>(acc + (uint32_t)c, v);
                 // the staging buffer is free once what went out of it two
-                // chunks ago has been read; with accumulation the next chunk's
-                // y is requested a chunk ahead
+                // chunks ago (in this tile or the one before) has been read;
+                // with accumulation the next chunk's y is requested a chunk ahead
                 if (e == 0) {
                     if (ACC) {
                         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
