@@ -521,11 +521,15 @@ class Int8Layer:
 
     def linear(self, rows: QuantRows, y, flags: int = 0, stream=None) -> None:
         """y (+)= W x for rows x; y is fp16, bf16 or float32 [T][M].  flags:
-        FLAG_ACCUMULATE, FLAG_EARLY_WEIGHTS (y's type is read off y)."""
+        FLAG_ACCUMULATE, FLAG_EARLY_WEIGHTS (y's type is read off y; a flag for
+        another type is refused)."""
         _, bf16, f32 = e = _floats()
         if rows.N != self.N or rows.device != self.device:
             raise ValueError(f"rows of {rows.N} codes on {rows.device} for a layer of {self.N} on {self.device}")
         ldy = _matrix(y, "y", (rows.T, self.M), e, self.device)
-        flags |= FLAG_BF16 if y.dtype == bf16 else FLAG_Y_FP32 if y.dtype == f32 else 0
+        kind = FLAG_BF16 if y.dtype == bf16 else FLAG_Y_FP32 if y.dtype == f32 else 0
+        if flags & (FLAG_BF16 | FLAG_Y_FP32) & ~kind:
+            raise ValueError(f"flags {flags} name another type than y's {y.dtype}")
+        flags |= kind
         _call("fluxbin_int8_linear", self.device, stream, self.M, self.N, self.w.data_ptr(), self.ldw,
               self.scale.data_ptr(), rows.q.data_ptr(), rows.ldq, rows.scale.data_ptr(), rows.T, y.data_ptr(), ldy, flags)
