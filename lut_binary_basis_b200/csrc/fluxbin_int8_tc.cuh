@@ -273,14 +273,16 @@ __device__ __forceinline__ int4 add4(const int4& a, const int4& b) {
 }
 
 // Tokens c, c + 8, .. below c1 of a split tile: the sums of `splits` <= MAX
-// CTAs, U tokens at a time, scaled and written.
+// CTAs, U tokens at a time, scaled and written.  Nothing read from another CTA
+// is left unused, so all of it has arrived when this returns: the lanes past
+// the end of M read from this CTA (`rank`).
 template <typename Y, bool ACC, int MAX, int U>
-__device__ __forceinline__ void int8_sum_split(const Int8Args& p, uint32_t ring, int splits, int64_t t0, int c, int c1,
-                                               int m0, int mq, const float (&sw4)[4], int failed) {
+__device__ __forceinline__ void int8_sum_split(const Int8Args& p, uint32_t ring, int splits, int rank, int64_t t0,
+                                               int c, int c1, int m0, int mq, const float (&sw4)[4], int failed) {
     constexpr int kWarps = kI8Threads / 32;
     uint32_t peer[MAX];
 #pragma unroll
-    for (int r = 0; r < MAX; ++r) peer[r] = dsmem_addr(ring + (uint32_t)(mq * 4), r < splits ? r : 0);
+    for (int r = 0; r < MAX; ++r) peer[r] = dsmem_addr(ring + (uint32_t)(mq * 4), r < splits && m0 + mq < p.M ? r : rank);
     for (; c < c1; c += U * kWarps) {
         int4 part[U][MAX];
 #pragma unroll
@@ -502,10 +504,16 @@ __global__ void __launch_bounds__(kI8Threads)
         // warp has the 128 channels of a token, four a lane, and the loads of
         // several tokens overlap
         const int c0 = nt * rank / a.splits, c1 = nt * (rank + 1) / a.splits;
-        if (a.splits <= 4)
-            int8_sum_split<Y, ACC, 4, 2>(p, ring, a.splits, t0, c0 + warp, c1, m0, mq, sw4, failed);
-        else
-            int8_sum_split<Y, ACC, kI8MaxSplits, 2>(p, ring, a.splits, t0, c0 + warp, c1, m0, mq, sw4, failed);
+        if (c0 + warp >= c1) {
+            // a warp without tokens has to wait for the word that it has read
+            // too: the barrier below orders no loads
+            if (failed) atomicOr(a.err, 1u);
+        } else if (a.splits <= 4) {
+            int8_sum_split<Y, ACC, 4, 2>(p, ring, a.splits, rank, t0, c0 + warp, c1, m0, mq, sw4, failed);
+        } else {
+            int8_sum_split<Y, ACC, kI8MaxSplits, 2>(p, ring, a.splits, rank, t0, c0 + warp, c1, m0, mq, sw4, failed);
+        }
+        __syncwarp();
         // the others have read this CTA's sums (nothing to publish: a release
         // would wait for the stores of y)
         asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
