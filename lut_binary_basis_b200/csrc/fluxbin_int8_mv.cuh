@@ -26,14 +26,16 @@ constexpr int kMvRows = 16, kMvWarps = 8, kMvTokens = 8;   // tokens of one inst
 constexpr int kMvSegment = 64;           // codes of K a warp takes at a time
 constexpr int kMvBatch = 8;              // segments in flight per warp
 
-// 16 codes from n on of a row of N (zeros past its end, whose bytes are not read).
+// 16 codes from n on of a row of N (zeros past its end, whose bytes are not
+// read).  STREAM: read once, so not kept in L1; not an invariant load, for the
+// preceding kernel may have written the row after this one started.
 template <bool STREAM>
 __device__ __forceinline__ uint4 mv_load(const int8_t* row, int n, int N) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (n + 16 <= N) {
         if (STREAM)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(row + n));
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(row + n) : "memory");
         else
             v = *reinterpret_cast<const uint4*>(row + n);
     } else if (n < N) {

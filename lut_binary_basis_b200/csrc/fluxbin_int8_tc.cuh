@@ -414,21 +414,23 @@ __global__ void __launch_bounds__(kI8Threads)
     }
     __syncwarp();
     // scales are read and outputs written after the preceding kernel; they
-    // are on their way while the products run
+    // are on their way while the products run.  (By plain loads: the preceding
+    // kernel writes them while this one is already running, so they are not
+    // what an invariant load may read.)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t t0 = (int64_t)tile_t * a.bn;
     const int nt = (int)(p.T - t0 < a.bn ? p.T - t0 : a.bn);
-    if (tid < a.bn) smem_at<float>(kI8SxOff + 4 * tid) = tid < nt ? __ldg(p.sx + t0 + tid) : 0.f;
+    if (tid < a.bn) smem_at<float>(kI8SxOff + 4 * tid) = tid < nt ? p.sx[t0 + tid] : 0.f;
     if (ACC && a.splits == 1 && tid < nt) int8_prefetch_row<Y>(p, t0 + tid, m0);
     const int quarter = warp & 3;                // the lanes of tensor memory that this warp reaches
     const int row = quarter * 32 + lane, m = m0 + row;
     const int mq = 4 * lane;                     // the four channels of the split's sums
     float sw4[4];
     if (a.splits == 1) {
-        sw4[0] = m < p.M ? __ldg(p.sw + m) : 0.f;
+        sw4[0] = m < p.M ? p.sw[m] : 0.f;
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sw4[j] = m0 + mq + j < p.M ? __ldg(p.sw + m0 + mq + j) : 0.f;
+        for (int j = 0; j < 4; ++j) sw4[j] = m0 + mq + j < p.M ? p.sw[m0 + mq + j] : 0.f;
     }
     // every thread waits for the accumulators; the full limit even under the
     // test hook, since nothing may release them under running instructions

@@ -365,10 +365,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
                 int8_tma(sb + buf0 + k * kI8PairOutBytes, &map_y, m0, (int)t0 + q * C, y_full + 8 * k);
             };
             // the tile's scales, requested before the accumulators are ready
-            const float sw = m < p.M ? __ldg(p.sw + m) : 0.f;
+            // (plain loads: the preceding kernel may have written them after
+            // this one started)
+            const float sw = m < p.M ? p.sw[m] : 0.f;
             {
                 const int c = tid - 64;
-                smem_at<float>(kI8PairSxOff + (b * kI8MaxBn + c) * 4) = c < a.bn && t0 + c < p.T ? __ldg(p.sx + t0 + c) : 0.f;
+                smem_at<float>(kI8PairSxOff + (b * kI8MaxBn + c) * 4) = c < a.bn && t0 + c < p.T ? p.sx[t0 + c] : 0.f;
             }
             if (ACC) {                             // (the tile before may have gone out by plain stores)
                 fence_async_smem();
