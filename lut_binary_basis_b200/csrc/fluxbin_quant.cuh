@@ -245,15 +245,24 @@ __device__ __forceinline__ void add_delta(Raw<float>& h, const Raw<E>& d) {
     }
 }
 
-__device__ __forceinline__ float silu(float g) {
-    // 2^(-g log2 e) overflows to infinity below g = -88 and its reciprocal is
-    // then 0: silu's own limit.  The approximate exponential and reciprocal are
-    // within a few 2^-23 of the value, far below half a step of 8 bits;
-    // flushing their subnormals saves the instructions that would scale them.
-    float e, rc;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + e));
-    return g * rc;
+// g / (1 + exp(-g)) of two gates, as g/4 divided by (1 + exp(-g)) / 4: the
+// approximate reciprocal gives 0 from 2^126 on, so that without the factor gates
+// below -87.33 would be lost, with it those below -88.72, where exp(-g) itself
+// leaves fp32 and the value is 0.  (g/4 is exact: a bf16 has no bit below 2^-133.)
+// The exponent's constant, product and difference are rounded, which the
+// exponential turns into a relative error of up to |g| + 1 units of 2^-23; the
+// approximate exponential, the sum, the reciprocal and the product add a few:
+// below 100 units, 2^-16, and half a step of 8 bits is 2^-8 of the row's maximum.
+// Flushing subnormals saves the instructions that would scale them.
+__device__ __forceinline__ uint64_t silu(uint64_t g) {
+    const float2 x = unpair(fma2(g, pair(-1.4426950408889634f, -1.4426950408889634f), pair(-2.f, -2.f)));
+    float2 e, rc;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
+    const float2 s = unpair(add2(pair(e.x, e.y), pair(0.25f, 0.25f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc.x) : "f"(s.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc.y) : "f"(s.y));
+    return mul2(mul2(g, pair(0.25f, 0.25f)), pair(rc.x, rc.y));
 }
 
 // A chunk's inputs.
@@ -312,10 +321,7 @@ __device__ __forceinline__ void quant_values(const QuantArgs& p, int64_t t, int 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             v[k] = widen(x.a, k);
-            if constexpr (KIND == kQuantSilu) {
-                const float2 g = unpair(v[k]);
-                v[k] = mul2(pair(silu(g.x), silu(g.y)), widen(x.b, k));
-            }
+            if constexpr (KIND == kQuantSilu) v[k] = mul2(silu(v[k]), widen(x.b, k));
         }
     }
 #pragma unroll
