@@ -11,7 +11,7 @@ from lut_binary_basis_b200 import fluxbin  # noqa: E402
 pytestmark = pytest.mark.gpu
 
 # the kernel for few tokens, split tiles, whole tiles, pairs (with one tile and with several)
-SHAPES = [(1, 700, 1000), (16, 4000, 2048), (9, 300, 9000), (40, 1000, 1500), (20, 30000, 512), (300, 9000, 500),
+SHAPES = [(1, 700, 1000), (16, 4000, 2048), (9, 300, 9000), (40, 1000, 1500), (1, 30000, 512), (20, 30000, 512), (300, 9000, 500),
           (448, 14336, 128)]
 
 
