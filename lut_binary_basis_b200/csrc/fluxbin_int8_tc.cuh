@@ -234,7 +234,7 @@ __device__ __forceinline__ void int8_rows_in(const Int8Args& p, uint32_t buf, in
                     if (off) hi[u] = *reinterpret_cast<const uint4*>(at - off + 16);
                 } else {
                     // the ends of the row; put where the shift below takes them from
-                    Y el[2 * kPer];
+                    alignas(16) Y el[2 * kPer];
 #pragma unroll
                     for (int k = 0; k < 2 * kPer; ++k) {
                         const int c = k - before;
