@@ -390,6 +390,9 @@ __global__ void __launch_bounds__(kI8Threads)
         // ---- matrix instructions ----
         if (elect_one()) {
             const uint32_t idesc = int8_idesc(kI8Rows, a.bn);
+            // the stages' tokens come after the preceding kernel, and the limit
+            // of a wait is not for that kernel's time
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             bool ok = true;
             int s = 0;
             uint32_t round = 0;
@@ -433,15 +436,15 @@ __global__ void __launch_bounds__(kI8Threads)
         for (int j = 0; j < 4; ++j) sw4[j] = m0 + mq + j < p.M ? p.sw[m0 + mq + j] : 0.f;
     }
     // every thread waits for the accumulators; the full limit even under the
-    // test hook, since nothing may release them under running instructions
-    const bool drained = aligned ? tc_mbar_wait(done, 0u, kI8SpinLimit) : true;
+    // test hook, since nothing may release them under running instructions.
+    // What one thread could not confirm, none takes for confirmed.
+    const bool drained = __syncthreads_and(!aligned || tc_mbar_wait(done, 0u, kI8SpinLimit)) != 0;
+    tc_fence_after();
+    const bool ok = drained && aligned && smem_at<const volatile uint32_t>(kFailed) == 0u;
     if (tid == 0 && (!drained || !aligned)) {
         atomicOr(a.err, drained ? 1u : 2u);
-        smem_at<uint32_t>(kFailed) = 1u;
+        smem_at<uint32_t>(kFailed) = 1u;         // (read by the cluster's other CTAs)
     }
-    __syncthreads();
-    tc_fence_after();
-    const bool ok = drained && smem_at<const volatile uint32_t>(kFailed) == 0u;
 
     const uint32_t acc0 = tmem + ((uint32_t)(quarter * 32) << 16);
     const bool bulk = a.splits == 1 && a.bulk > (p.M - m0 >= kI8Rows ? 0 : 1);

@@ -309,6 +309,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
         if (rank == 0 && aligned && elect_one()) {
             // ---- matrix instructions, for both CTAs ----
             const uint32_t idesc = int8_idesc(2 * kI8Rows, a.bn);
+            // the stages' tokens come after the preceding kernel, and the limit
+            // of a wait is not for that kernel's time
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             int s = 0;
             uint32_t round = 0;
             int64_t n = 0;                         // tiles so far
@@ -457,15 +460,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8PairThreads, 1)
             if (lane == 0) int8_remote_arrive(dsmem_addr(acc_empty0 + 8 * b, 0));
         }
         if (a.bulk && e == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        if (!ok && lane == 0) atomicOr(a.err, 1u);
+        if (!ok) atomicOr(a.err, 1u);
     }
+    // every role has come to its end before anyone waits for the last matrix
+    // instructions: the limit of that wait is not for all of the tiles' time
     __syncwarp();
-    const bool drained = aligned ? tc_mbar_wait(done, 0u, kI8SpinLimit) : true;
-    if (!drained && tid == 0) atomicOr(a.err, 2u);
+    __syncthreads();
+    const bool drained = !aligned || tc_mbar_wait(done, 0u, kI8SpinLimit);
     tc_fence_before();
-    // the release takes both CTAs: each knows whether the other's wait went well
+    // the release takes both CTAs: each knows whether the other's waits went well
     const int all_drained = __syncthreads_and(drained);
-    if (tid == 0) smem_at<int>(kDrained) = all_drained;
+    if (tid == 0) {
+        smem_at<int>(kDrained) = all_drained;
+        if (!all_drained || !aligned) atomicOr(a.err, all_drained ? 1u : 2u);
+    }
     int8_cluster_sync();
     const bool release = all_drained && ld_dsmem(dsmem_addr(sb + kDrained, rank ^ 1)) != 0;
     int8_cluster_sync();
