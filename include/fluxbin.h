@@ -401,7 +401,8 @@ int fluxbin_linear_static_scratch(const fluxbin_layer_desc* desc,
  *   with it is NaN.
  *
  * Rows may be apart: every array of rows has a pitch (ld..., in elements, at
- * least the row's length and at most 2^39).  Arrays of codes start at a
+ * least the row's length and at most 2^39; no more than 2^57 bytes from the first
+ * row to the last).  Arrays of codes start at a
  * multiple of 16 bytes and have a pitch that is a multiple of 16; the bytes
  * between two rows are neither read nor written.  Other arrays need the
  * alignment of their elements only (16-byte aligned rows of a length that is

@@ -22,10 +22,14 @@ namespace {
 constexpr int32_t kInt8MaxN = 131071;   // 128 * 128 * N < 2^31
 constexpr int32_t kInt8MaxRows = INT32_MAX - 1023;   // a tile's last row still has a 32-bit number
 
-constexpr int64_t kMaxPitch = (int64_t)1 << 39;   // beyond any device memory: offsets stay far from 2^63
+// Beyond any address space: offsets and sums of them stay far from 2^63.
+constexpr int64_t kMaxPitch = (int64_t)1 << 39;   // elements from a row to the next
+constexpr int64_t kMaxSpan = (int64_t)1 << 57;    // bytes from the first row to the last
 
-// A row pitch (in elements) that rows of n elements can have.
-bool bad_pitch(int64_t ld, int64_t n) { return ld < n || ld > kMaxPitch; }
+// A row pitch (in elements of `size` bytes) that T rows of n elements can have.
+bool bad_pitch(int64_t ld, int64_t n, int64_t T, int64_t size) {
+    return ld < n || ld > kMaxPitch || (T > 1 && ld * size > kMaxSpan / (T - 1));
+}
 
 bool ptr_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -522,7 +526,7 @@ extern "C" {
 int fluxbin_quant_rows(int32_t T, int32_t N, const uint16_t* d_x, int64_t ldx, int8_t* d_q, int64_t ldq,
                        float* d_scale, uint32_t flags, void* stream) {
     if (flags & ~FLUXBIN_FLAG_BF16) return FLUXBIN_ERR_INVALID_ARG;
-    if (T < 0 || N < 0 || bad_pitch(ldx, N) || bad_pitch(ldq, N)) return FLUXBIN_ERR_BAD_SHAPE;
+    if (T < 0 || N < 0 || bad_pitch(ldx, N, T, 2) || bad_pitch(ldq, N, T, 1)) return FLUXBIN_ERR_BAD_SHAPE;
     if (T == 0) return FLUXBIN_OK;
     return run_quant<kQuantQuant>(Rows{d_x, T, N, ldx, 2}, Rows{nullptr, T, N, 0, 2}, nullptr, 0.f,
                                   Rows{nullptr, T, N, 0, 2}, d_q, ldq, d_scale, flags, stream);
@@ -531,7 +535,8 @@ int fluxbin_quant_rows(int32_t T, int32_t N, const uint16_t* d_x, int64_t ldx, i
 int fluxbin_silu_mul_quant(int32_t T, int32_t N, const uint16_t* d_gate, int64_t ldg, const uint16_t* d_up,
                            int64_t ldu, int8_t* d_q, int64_t ldq, float* d_scale, uint32_t flags, void* stream) {
     if (flags & ~FLUXBIN_FLAG_BF16) return FLUXBIN_ERR_INVALID_ARG;
-    if (T < 0 || N < 0 || bad_pitch(ldg, N) || bad_pitch(ldu, N) || bad_pitch(ldq, N)) return FLUXBIN_ERR_BAD_SHAPE;
+    if (T < 0 || N < 0 || bad_pitch(ldg, N, T, 2) || bad_pitch(ldu, N, T, 2) || bad_pitch(ldq, N, T, 1))
+        return FLUXBIN_ERR_BAD_SHAPE;
     if (T == 0) return FLUXBIN_OK;
     return run_quant<kQuantSilu>(Rows{d_gate, T, N, ldg, 2}, Rows{d_up, T, N, ldu, 2}, nullptr, 0.f,
                                  Rows{nullptr, T, N, 0, 2}, d_q, ldq, d_scale, flags, stream);
@@ -542,12 +547,12 @@ int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, co
                           float* d_scale, uint32_t flags, void* stream) {
     if (flags & ~(FLUXBIN_FLAG_BF16 | FLUXBIN_FLAG_H_FP32)) return FLUXBIN_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return FLUXBIN_ERR_INVALID_ARG;
-    if (T < 0 || N < 0 || bad_pitch(ldh, N) || bad_pitch(ldq, N) || (d_delta && bad_pitch(ldd, N)) ||
-        (d_h_out && bad_pitch(ldo, N)))
+    const int hs = (flags & FLUXBIN_FLAG_H_FP32) ? 4 : 2;
+    if (T < 0 || N < 0 || bad_pitch(ldh, N, T, hs) || bad_pitch(ldq, N, T, 1) ||
+        (d_delta && bad_pitch(ldd, N, T, 2)) || (d_h_out && bad_pitch(ldo, N, T, hs)))
         return FLUXBIN_ERR_BAD_SHAPE;
     if (T == 0) return FLUXBIN_OK;
     if (N == 0) return FLUXBIN_ERR_BAD_SHAPE;   // no mean of h^2 to take
-    const int hs = (flags & FLUXBIN_FLAG_H_FP32) ? 4 : 2;
     return run_quant<kQuantNorm>(Rows{d_h, T, N, ldh, hs}, Rows{d_delta, T, N, ldd, 2}, d_gamma, eps,
                                  Rows{d_h_out, T, N, ldo, hs}, d_q, ldq, d_scale, flags, stream);
 }
@@ -559,12 +564,12 @@ int fluxbin_int8_linear(int32_t M, int32_t N, const int8_t* d_w, int64_t ldw, co
                   FLUXBIN_FLAG_TEST_WAIT_TIMEOUT))
         return FLUXBIN_ERR_INVALID_ARG;
     if ((flags & FLUXBIN_FLAG_Y_FP32) && (flags & FLUXBIN_FLAG_BF16)) return FLUXBIN_ERR_INVALID_ARG;
-    if (M < 0 || N < 0 || T < 0 || bad_pitch(ldw, N) || bad_pitch(ldx, N) || bad_pitch(ldy, M))
+    const int ys = (flags & FLUXBIN_FLAG_Y_FP32) ? 4 : 2;
+    if (M < 0 || N < 0 || T < 0 || bad_pitch(ldw, N, M, 1) || bad_pitch(ldx, N, T, 1) || bad_pitch(ldy, M, T, ys))
         return FLUXBIN_ERR_BAD_SHAPE;
     if (N > kInt8MaxN || M > kInt8MaxRows || T > kInt8MaxRows) return FLUXBIN_ERR_UNSUPPORTED;
     if (M == 0 || T == 0) return FLUXBIN_OK;
     if (!d_y || !d_wscale || !d_xscale || (N > 0 && (!d_w || !d_x))) return FLUXBIN_ERR_INVALID_ARG;
-    const int ys = (flags & FLUXBIN_FLAG_Y_FP32) ? 4 : 2;
     if (!ptr_aligned(d_y, ys) || !ptr_aligned(d_wscale, 4) || !ptr_aligned(d_xscale, 4) || !ptr_aligned(d_w, 16) ||
         !ptr_aligned(d_x, 16) || ldw % 16 || ldx % 16)
         return FLUXBIN_ERR_MISALIGNED;
