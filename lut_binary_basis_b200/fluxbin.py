@@ -508,16 +508,21 @@ class Int8Layer:
     @classmethod
     def from_host(cls, W: np.ndarray, device="cuda") -> "Int8Layer":
         """Quantise a dense host matrix W [M][N] per row (the formula of the
-        8-bit operators, in fp64) and copy it to ``device``."""
+        8-bit operators, in fp64) and copy it to ``device``.  A row whose scale
+        is 0 in fp32 is a row of zeros; one beyond fp32 is refused."""
         import torch
         W = np.asarray(W, dtype=np.float64)
         M, N = W.shape
         if not np.all(np.isfinite(W)):
             raise ValueError("W has a NaN or an infinity in it")
         a = np.abs(W).max(axis=1, initial=0.0)
+        with np.errstate(over="ignore"):
+            scale = (a / 127.0).astype(np.float32)
+        if not np.all(np.isfinite(scale)):
+            raise ValueError("a row of W has a scale beyond fp32")
         q = np.zeros((M, _pitch16(N)), np.int8)
-        q[:, :N] = np.rint(W * np.divide(127.0, a, out=np.zeros(M), where=a > 0)[:, None])
-        return cls(torch.from_numpy(q).to(device)[:, :N], torch.from_numpy((a / 127.0).astype(np.float32)).to(device))
+        q[:, :N] = np.rint(W * np.divide(127.0, a, out=np.zeros(M), where=scale > 0)[:, None])
+        return cls(torch.from_numpy(q).to(device)[:, :N], torch.from_numpy(scale).to(device))
 
     def linear(self, rows: QuantRows, y, flags: int = 0, stream=None) -> None:
         """y (+)= W x for rows x; y is fp16, bf16 or float32 [T][M].  flags:
