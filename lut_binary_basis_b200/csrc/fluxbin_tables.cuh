@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kTabThreads) fluxbin_tables_kernel(const Kerne
             // 16-byte loads of 8 entries
             const uint4* h8 = reinterpret_cast<const uint4*>(a.x);
             for (int n = tid; n < a.N / 8; n += kTabThreads) {
-                const uint4 w = __ldg(h8 + n);
+                const uint4 w = h8[n];      // (the preceding kernel's output: not an invariant load)
                 const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

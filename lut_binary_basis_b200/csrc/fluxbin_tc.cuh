@@ -320,8 +320,8 @@ __device__ __forceinline__ void tc_prod_load(const TcArgs& a, int u, int tid, Tc
         const int n0 = t.ul * P * MU + kk0 % (P * MU);
         if (!t.br && !t.gather && a.vec_x && n0 + 8 <= t.ncols) {
             o.c = __ldg(reinterpret_cast<const uint4*>(t.c + (int64_t)k * t.ncols + n0));
-            o.x = b < a.B ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)b * a.N + n0))
-                          : make_uint4(0, 0, 0, 0);
+            // (x is the preceding kernel's output: a plain load, not an invariant one)
+            o.x = b < a.B ? *reinterpret_cast<const uint4*>(a.x + (int64_t)b * a.N + n0) : make_uint4(0, 0, 0, 0);
             return;
         }
         uint32_t c[4] = {0u, 0u, 0u, 0u}, x[4] = {0u, 0u, 0u, 0u};
