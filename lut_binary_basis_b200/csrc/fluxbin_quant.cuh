@@ -249,20 +249,21 @@ __device__ __forceinline__ void add_delta(Raw<float>& h, const Raw<E>& d) {
 // approximate reciprocal gives 0 from 2^126 on, so that without the factor gates
 // below -87.33 would be lost, with it those below -88.72, where exp(-g) itself
 // leaves fp32 and the value is 0.  (g/4 is exact: a bf16 has no bit below 2^-133.)
-// The exponent's constant, product and difference are rounded, which the
-// exponential turns into a relative error of up to |g| + 1 units of 2^-23; the
-// approximate exponential, the sum, the reciprocal and the product add a few:
-// below 100 units, 2^-16, and half a step of 8 bits is 2^-8 of the row's maximum.
+// The exponent's constant and product are rounded, which the exponential turns
+// into a relative error of up to |g| units of 2^-23; the approximate
+// exponential, the sum, the reciprocal and the product add a few: below 100
+// units, 2^-16, and half a step of 8 bits is 2^-8 of the row's maximum.
 // Flushing subnormals saves the instructions that would scale them.
 __device__ __forceinline__ uint64_t silu(uint64_t g) {
-    const float2 x = unpair(fma2(g, pair(-1.4426950408889634f, -1.4426950408889634f), pair(-2.f, -2.f)));
+    const uint64_t quarter = pair(0.25f, 0.25f);
+    const float2 x = unpair(mul2(g, pair(-1.4426950408889634f, -1.4426950408889634f)));
     float2 e, rc;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
-    const float2 s = unpair(add2(pair(e.x, e.y), pair(0.25f, 0.25f)));
+    const float2 s = unpair(fma2(pair(e.x, e.y), quarter, quarter));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc.x) : "f"(s.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc.y) : "f"(s.y));
-    return mul2(mul2(g, pair(0.25f, 0.25f)), pair(rc.x, rc.y));
+    return mul2(mul2(g, quarter), pair(rc.x, rc.y));
 }
 
 // A chunk's inputs.

@@ -3,9 +3,9 @@ fp32 holds (down to g = -88.72; 1 + exp(-g) has no normal reciprocal from
 -87.33 on), and below, where the value is 0.
 
 Tolerance.  v = g / (1 + exp(-g)) u is held to a relative delta, in units of
-2^-23: the exponent's rounded constant, product and difference turn into |g| + 1,
-the approximate exponential has 2, the sum, the reciprocal and two products
-add 3 at most: delta = (|g| + 6) 2^-23.  A code is within 1/2 of v / s up to 127
+2^-23: the exponent's rounded constant and product turn into |g|, the approximate
+exponential has 2, the sum, the reciprocal and two products add 3 at most:
+delta = (|g| + 5) 2^-23.  A code is within 1/2 of v / s up to 127
 times its own error and the maximum's; the scale has the maximum's error and one
 rounding.
 """
@@ -36,7 +36,7 @@ def check(g, u, rows):
     gate, up = (t.float().cpu().numpy().astype(np.float64) for t in (g, u))
     with np.errstate(over="ignore"):
         v = np.where(gate < LIMIT, 0.0, gate / (1.0 + np.exp(-gate)) * up)
-    delta = (np.abs(np.maximum(gate, LIMIT)) + 6) * 2.0 ** -23
+    delta = (np.abs(np.maximum(gate, LIMIT)) + 5) * 2.0 ** -23
     a = np.abs(v).max(axis=1)
     delta_max = delta.max(axis=1)
     s = rows.scale.cpu().numpy().astype(np.float64)
