@@ -402,9 +402,9 @@ int fluxbin_linear_static_scratch(const fluxbin_layer_desc* desc,
  *
  * Rows may be apart: every array of rows has a pitch (ld..., in elements, at
  * least the row's length and at most 2^39; no more than 2^57 bytes from the first
- * row to the last).  Arrays of codes start at a
- * multiple of 16 bytes and have a pitch that is a multiple of 16; the bytes
- * between two rows are neither read nor written.  Other arrays need the
+ * row to the last).  Arrays of codes start at a multiple of 16 bytes and have a
+ * pitch that is a multiple of 16; the bytes between two rows are neither read
+ * nor written.  Other arrays need the
  * alignment of their elements only (16-byte aligned rows of a length that is
  * a multiple of 8 are faster).  16-bit values are fp16, or bfloat16 with
  * FLUXBIN_FLAG_BF16.  Outputs must not overlap each other or an input (the
@@ -451,9 +451,9 @@ int fluxbin_silu_mul_quant(int32_t T, int32_t N, const uint16_t* d_gate, int64_t
  *   d_h_out  [T][ldo] of h's type or NULL: receives h'; may be d_h itself (with ldo == ldh)
  *   d_q, d_scale   as for fluxbin_quant_rows
  *   flags    FLUXBIN_FLAG_BF16, FLUXBIN_FLAG_H_FP32
- * The sum of squares is taken in fp32 in a fixed order; a row whose sum, or
- * whose 1/rms (a row of zeros with eps == 0), is not finite has no finite
- * scale (above).  N == 0 is BAD_SHAPE.
+ * The products h' gamma and the sum of squares are taken in fp32, the sum in a
+ * fixed order; a row whose products or sum, or whose 1/rms (a row of zeros with
+ * eps == 0), is not finite has no finite scale (above).  N == 0 is BAD_SHAPE.
  * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
  */
 int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, const uint16_t* d_delta, int64_t ldd,
@@ -472,8 +472,9 @@ int fluxbin_rmsnorm_quant(int32_t T, int32_t N, const void* d_h, int64_t ldh, co
  *   d_x      int8 codes [T][ldx], d_xscale float32 [T]; any T >= 0
  *   d_y      [T][ldy]: fp16, bfloat16 (FLUXBIN_FLAG_BF16) or float32 (FLUXBIN_FLAG_Y_FP32)
  *   flags    FLUXBIN_FLAG_ACCUMULATE, FLUXBIN_FLAG_Y_FP32, FLUXBIN_FLAG_BF16 (not both types),
- *            FLUXBIN_FLAG_EARLY_WEIGHTS (w may be read before the preceding kernel on the
- *            stream has finished), FLUXBIN_FLAG_TEST_WAIT_TIMEOUT (test hook: the kernel's
+ *            FLUXBIN_FLAG_EARLY_WEIGHTS (w may be read before the preceding kernels on the
+ *            stream have finished: no kernel still running before this call writes it),
+ *            FLUXBIN_FLAG_TEST_WAIT_TIMEOUT (test hook: the kernel's
  *            copies are never issued and its waits give up after a few polls: the outputs
  *            become NaN and bit 0 of fluxbin_device_status is set)
  * M and T are at most 2^31 - 1024 (UNSUPPORTED above).  M == 0 returns FLUXBIN_OK

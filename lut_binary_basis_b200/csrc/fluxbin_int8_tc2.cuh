@@ -28,7 +28,7 @@
 // memory.
 //
 // Bound: the tensor cores, 96% busy while an SM has a tile (2048x28672x8192:
-// 294 to 332 us with the GPU's power cap, 2.9 to 3.3 POP/s; the last of 13
+// 285 to 332 us with the GPU's power cap, 2.9 to 3.4 POP/s; the last of 13
 // rounds has 8 tiles for 74 pairs).
 #pragma once
 

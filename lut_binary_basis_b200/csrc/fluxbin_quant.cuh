@@ -35,8 +35,8 @@
 // memory stays busy while the resident CTAs compute and store.
 // Measured (B200, a graph of calls on rotated inputs): norm with residual
 // 2048x8192 fp16 20 us, 89% of the measured copy rate, 2047x4099 22 (41%);
-// quant 4096x8192 17.0 (91%), 4096x8191 33 (47%); gate 2048x11008 22.5 (77%),
-// 2048x28672 52 (87%), 2048x28671 98 (46%).
+// quant 4096x8192 17.0 (91%), 4096x8191 33 (47%); gate 2048x11008 22.3 (78%),
+// 2048x28672 52 (87%), 2048x28671 100 (45%).
 #pragma once
 
 #include <cuda_bf16.h>
