@@ -434,7 +434,7 @@ int fluxbin_quant_rows(int32_t T, int32_t N, const uint16_t* d_x, int64_t ldx, i
  *   v[n] = g[n] / (1 + exp(-g[n])) * u[n]
  * in fp32 from 16-bit g and u (d_gate and d_up may be the two halves of the
  * rows of one array).  Below g = -88.72 exp(-g) is beyond fp32 and v is 0; above,
- * v is off by at most |g| + 5 units of 2^-23.  Other arguments as for fluxbin_quant_rows.
+ * the relative error of v is at most (|g| + 5) 2^-23.  Other arguments as for fluxbin_quant_rows.
  * Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, UNSUPPORTED, CUDA.
  */
 int fluxbin_silu_mul_quant(int32_t T, int32_t N, const uint16_t* d_gate, int64_t ldg, const uint16_t* d_up,
